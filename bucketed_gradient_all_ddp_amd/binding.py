@@ -45,8 +45,12 @@ EXPORTS = [
     "allreduce_sim", "allreduce_sim_workspace", "ddp_schedule_time", "ddp_choose_schedule",
     "ddp_overlap_step_time",
     "reduce_scatter_sim", "allgather_sim", "broadcast_sim",
+    "ddp_grad_norm_workspace", "ddp_grad_norm", "ddp_clip_grads", "ddp_sync_norm_workspace",
+    "ddp_allreduce_buckets_norm", "ddp_grad_norm_finish", "ddp_allreduce_clip",
+    "ddp_reducer_set_norm",
 ]
 
+NORM = {"l2": 0, "l1": 1, "inf": 2}
 SCHEDULES = {"ring": 0, "recursive_doubling": 1, "rabenseifner": 2, "tree": 3}
 
 
@@ -139,6 +143,16 @@ def load_library(path: str = LIB_PATH):
         "reduce_scatter_sim": ([vp, vp, i32, i64, i32, i32, vp, vp, vp], st),
         "allgather_sim": ([vp, vp, i32, i64, i32, vp, vp], st),
         "broadcast_sim": ([vp, i32, i64, i32, i32, vp, vp], st),
+        "ddp_grad_norm_workspace": ([vp, i32], sz),
+        "ddp_grad_norm": ([vp, i32, vp, i32, i32, vp, vp, vp, sz, vp], st),
+        "ddp_clip_grads": ([vp, i32, vp, i32, vp, i32, f32, f32, i32, vp], st),
+        "ddp_sync_norm_workspace": ([vp], sz),
+        "ddp_allreduce_buckets_norm": ([vp, i32, i32, i32, vp, i32, i32, vp, i32, vp, sz, vp, vp],
+                                       st),
+        "ddp_grad_norm_finish": ([vp, i32, vp, vp, vp, sz, vp], st),
+        "ddp_allreduce_clip": ([vp, i32, vp, i32, i32, vp, i32, f32, f32, vp, vp, vp, sz, vp, vp],
+                               st),
+        "ddp_reducer_set_norm": ([vp, i32, vp, sz], st),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -317,6 +331,15 @@ class Plan:
     def segment_bytes(self, p: int) -> int:
         return load_library().ddp_plan_segment_bytes(self._h, p)
 
+    def grad_norm_workspace(self, p: int) -> int:
+        """Workspace bytes of ddp_grad_norm over p ranks."""
+        return load_library().ddp_grad_norm_workspace(self._h, p)
+
+    def sync_norm_workspace(self) -> int:
+        """Workspace bytes of ddp_allreduce_buckets_norm, ddp_grad_norm_finish
+        and ddp_allreduce_clip."""
+        return load_library().ddp_sync_norm_workspace(self._h)
+
     # A re-upload replaces a device table that kernels already enqueued may
     # still read, possibly on other streams (the reducer's communication
     # stream): the old table is released only after the device has drained.
@@ -466,6 +489,7 @@ def grad_pointer_table(grads: Sequence[Sequence], device="cuda"):
     table._ddp_ranks = len(grads)
     table._ddp_numel = tuple(g.numel() for g in first)
     table._ddp_elem_bytes = first[0].element_size() if first else 0
+    table._ddp_dtypes = frozenset(g.dtype for rank in grads for g in rank)
     return table
 
 
@@ -588,6 +612,188 @@ def ddp_allreduce_buckets(plan: Plan, first_bucket: int, n_buckets: int, grad_ta
     return st
 
 
+# ---------------------------------------------------------------------------
+# Gradient norm and clipping
+# ---------------------------------------------------------------------------
+
+def _on_device(tensor):
+    """The library launches on the current device: make that the tensor's."""
+    import contextlib
+
+    import torch
+
+    if tensor is None or tensor.device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(tensor.device)
+
+
+def _empty(n: int, dtype, device, stream):
+    """Device memory for use on `stream` (None: the current stream)."""
+    import torch
+
+    if stream is None:
+        return torch.empty(n, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=dtype, device=device)
+
+
+def _check_norm_dtype(table, what: str) -> None:
+    """The norm and clip kernels read values, not bytes: float32 or bfloat16
+    gradients, all of one type."""
+    import torch
+
+    dtypes = getattr(table, "_ddp_dtypes", None)
+    if dtypes and dtypes not in ({torch.float32}, {torch.bfloat16}):
+        raise TypeError(f"{what}: gradients must all be float32 or all bfloat16, got "
+                        f"{sorted(map(str, dtypes))}")
+
+
+def _floats(t, n: int, device, what: str, name: str) -> Optional[int]:
+    """Address of a contiguous float32 device tensor of n elements."""
+    import torch
+
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{what}: {name} must be a contiguous float32 tensor of {n} elements")
+    ptr = _device_ptr(t)
+    if device is not None and t.device != device:
+        raise ValueError(f"{what}: {name} is on {t.device}, the gradient table on {device}")
+    return ptr
+
+
+def _workspace(t, table, what: str) -> Tuple[Optional[int], int]:
+    if t is None:
+        return None, 0
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: the workspace must be contiguous")
+    ptr = _device_ptr(t)
+    if table is not None and t.device != table.device:
+        raise ValueError(f"{what}: the workspace is on {t.device}, the gradient table on "
+                         f"{table.device}")
+    return ptr, t.numel() * t.element_size()
+
+
+def _plan_dtype(plan: Plan) -> int:
+    return DTYPE_F32 if plan.elem_bytes == 4 else DTYPE_BF16
+
+
+def ddp_grad_norm(plan: Plan, grad_table, p: int, norms=None, norm_type: str = "l2",
+                  param_norms=None, ranks: Optional[Tuple[int, int]] = None, workspace=None,
+                  stream=None):
+    """The norm ("l2", "l1" or "inf") of each rank's gradients over all
+    parameters, as a float32 device tensor (`norms`, or a new one). `ranks`
+    = (first, count) takes some of the table's p ranks. `param_norms`, if
+    given, is a float32 tensor [count, n_params] that receives every
+    gradient's own norm."""
+    import torch
+
+    what = "ddp_grad_norm"
+    _check_grad_table(grad_table, plan, p, what)
+    _check_norm_dtype(grad_table, what)
+    first, count = (0, p) if ranks is None else ranks
+    if first < 0 or count < 1 or first + count > p:
+        raise ValueError(f"{what}: ranks {first}..{first + count - 1} outside 0..{p - 1}")
+    device = grad_table.device if grad_table is not None else None
+    with _on_device(grad_table):
+        if norms is None:
+            norms = _empty(count, torch.float32, device, stream)
+        if workspace is None:
+            workspace = _empty(max(16, plan.grad_norm_workspace(count)), torch.uint8, device,
+                               stream)
+        out = _floats(norms, count, device, what, "norms")
+        each = _floats(param_norms, count * plan.num_params, device, what, "param_norms")
+        ws, ws_bytes = _workspace(workspace, grad_table, what)
+        table = _device_ptr(grad_table) + 8 * first * plan.num_params if device else None
+        _check(load_library().ddp_grad_norm(plan.handle, count, table, _plan_dtype(plan),
+                                            NORM[norm_type], out, each, ws, ws_bytes,
+                                            _stream(stream)), what)
+    return norms
+
+
+def ddp_clip_grads(plan: Plan, grad_table, p: int, norms, max_norm: float, eps: float = 1e-6,
+                   replicated: bool = False, stream=None) -> None:
+    """Scale every gradient in place by min(1, max_norm / (norm + eps)).
+    `norms`: a float32 device tensor of one norm, or of one per rank.
+    `replicated`: every rank holds rank 0's gradients (as after an
+    all-reduce), which are read once and written to all."""
+    what = "ddp_clip_grads"
+    _check_grad_table(grad_table, plan, p, what)
+    _check_norm_dtype(grad_table, what)
+    device = grad_table.device if grad_table is not None else None
+    n = 1 if norms.numel() == 1 or replicated else p
+    with _on_device(grad_table):
+        _check(load_library().ddp_clip_grads(
+            plan.handle, p, _device_ptr(grad_table) if device else None, _plan_dtype(plan),
+            _floats(norms, n, device, what, "norms"), n, max_norm, eps, 1 if replicated else 0,
+            _stream(stream)), what)
+
+
+def ddp_allreduce_buckets_norm(plan: Plan, first_bucket: int, n_buckets: int, grad_table, p: int,
+                               workspace, norm_type: str = "l2", avg: str = "none", tokens=None,
+                               stream=None) -> CommStats:
+    """ddp_allreduce_buckets that also leaves the norm's partial sums of the
+    averaged gradients in `workspace` (plan.sync_norm_workspace() bytes);
+    ddp_grad_norm_finish joins them once every bucket has been reduced."""
+    what = "ddp_allreduce_buckets_norm"
+    _check_grad_table(grad_table, plan, p, what)
+    _check_norm_dtype(grad_table, what)
+    st = CommStats()
+    with _on_device(grad_table):
+        ws, ws_bytes = _workspace(workspace, grad_table, what)
+        _check(load_library().ddp_allreduce_buckets_norm(
+            plan.handle, first_bucket, n_buckets, p,
+            _device_ptr(grad_table) if grad_table is not None else None, _plan_dtype(plan),
+            AVG[avg], _tokens(tokens, p), NORM[norm_type], ws, ws_bytes, _stream(stream),
+            ctypes.byref(st)), what)
+    return st
+
+
+def ddp_grad_norm_finish(plan: Plan, workspace, norm=None, norm_type: str = "l2",
+                         param_norms=None, stream=None):
+    """The norm whose partial sums ddp_allreduce_buckets_norm (or a reducer
+    with set_norm) left in `workspace`, as a float32 device tensor of one
+    element (`norm`, or a new one); `param_norms`, if given, receives the
+    n_params norms of the single parameters."""
+    import torch
+
+    what = "ddp_grad_norm_finish"
+    device = workspace.device
+    with _on_device(workspace):
+        if norm is None:
+            norm = _empty(1, torch.float32, device, stream)
+        ws, ws_bytes = _workspace(workspace, None, what)
+        _check(load_library().ddp_grad_norm_finish(
+            plan.handle, NORM[norm_type], _floats(norm, 1, device, what, "norm"),
+            _floats(param_norms, plan.num_params, device, what, "param_norms"), ws, ws_bytes,
+            _stream(stream)), what)
+    return norm
+
+
+def ddp_allreduce_clip(plan: Plan, grad_table, p: int, max_norm: float, norm, workspace,
+                       eps: float = 1e-6, norm_type: str = "l2", avg: str = "none", tokens=None,
+                       param_norms=None, stream=None) -> CommStats:
+    """All-reduce every bucket, take the norm of the averaged gradient (into
+    `norm`, a float32 device tensor of one element) and clip by it: every
+    rank ends with min(1, max_norm / (norm + eps)) times the average."""
+    what = "ddp_allreduce_clip"
+    _check_grad_table(grad_table, plan, p, what)
+    _check_norm_dtype(grad_table, what)
+    device = grad_table.device if grad_table is not None else None
+    st = CommStats()
+    with _on_device(grad_table):
+        ws, ws_bytes = _workspace(workspace, grad_table, what)
+        _check(load_library().ddp_allreduce_clip(
+            plan.handle, p, _device_ptr(grad_table) if device else None, _plan_dtype(plan),
+            AVG[avg], _tokens(tokens, p), NORM[norm_type], max_norm, eps,
+            _floats(norm, 1, device, what, "norm"),
+            _floats(param_norms, plan.num_params, device, what, "param_norms"), ws, ws_bytes,
+            _stream(stream), ctypes.byref(st)), what)
+    return st
+
+
 class Reducer:
     """Owner of a ddp_reducer: bucket all-reduces launched on `comm_stream`
     as parameters are marked ready (see include/ddpsim.h)."""
@@ -630,6 +836,17 @@ class Reducer:
         """Cap each all-reduce launch at n workgroups (0: one per tile)."""
         _check(load_library().ddp_reducer_set_max_workgroups(self._h, n),
                "ddp_reducer_set_max_workgroups")
+
+    def set_norm(self, workspace, norm_type: str = "l2") -> None:
+        """Have every launch leave the norm's partial sums in `workspace`
+        (plan.sync_norm_workspace() bytes) for ddp_grad_norm_finish after
+        finalize; None: no norm."""
+        if workspace is not None:
+            _check_norm_dtype(self._table, "Reducer.set_norm")
+        ptr, nbytes = _workspace(workspace, self._table, "Reducer.set_norm")
+        _check(load_library().ddp_reducer_set_norm(self._h, NORM[norm_type], ptr, nbytes),
+               "ddp_reducer_set_norm")
+        self._workspace = workspace  # kept alive
 
     def ready_order(self) -> List[int]:
         """Parameters in the order they were marked ready this (or the last)

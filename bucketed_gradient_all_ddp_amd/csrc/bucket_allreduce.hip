@@ -22,10 +22,16 @@
 // skips the first d loads and adds them at the end, which is its own ring
 // order. Tiles are therefore whole parameters cut into 64-vector runs, with
 // no lanes left idle at chunk ends.
+//
+// The same pass can also take the norm of the averaged gradient, one partial
+// sum per tile, from the fp32 values before they are rounded to the
+// gradients' type, and it can scale them by the clip coefficient of a norm
+// in device memory (SyncMode).
 #include <algorithm>
 
 #include "fold.hpp"
 #include "internal.hpp"
+#include "norm.hpp"
 
 namespace ddpsim {
 int32_t plan_num_buckets(const ddp_plan *plan);
@@ -111,14 +117,29 @@ __device__ __forceinline__ void fold_vector_per_lane(uint64_t mine, int32_t p, i
   }
 }
 
+// What happens to a finished fp32 value on its way to the ranks: kMode as
+// SyncMode, `sum` this lane's part of the tile's norm, `scale` the clip
+// coefficient.
+template <int kMode, int NT>
+struct TileEpilogue {
+  static constexpr bool kStore = kMode != kFoldNorm;
+  NormSum<NT> sum;
+  float scale = 1.0f;
+  __device__ __forceinline__ float operator()(float y) {
+    if constexpr (kMode == kSyncNorm || kMode == kFoldNorm) sum.add(y);
+    if constexpr (kMode == kSyncScale) y = y * scale;
+    return y;
+  }
+};
+
 // One tile of the plan's numbering; the tile map names the parameter
 // descriptor (index into seg) each tile belongs to.
-template <typename Tr, int VPT, int RB, bool kNT>
+template <typename Tr, int VPT, int RB, bool kNT, typename Epilogue>
 __device__ __forceinline__ void bucket_tile(const SegDesc *__restrict__ seg,
                                             const int32_t *__restrict__ tile_seg,
                                             int64_t map_stride, int32_t tile, int32_t n_params,
                                             const void *const *__restrict__ grads, int32_t p,
-                                            const Divide &div) {
+                                            const Divide &div, Epilogue &epi) {
   constexpr int V = Tr::kVec;
   constexpr int64_t kElemBytes = sizeof(typename Tr::elem);
   const SegDesc d = seg[tile_seg[tile_map_index(tile, map_stride)]];
@@ -145,8 +166,9 @@ __device__ __forceinline__ void bucket_tile(const SegDesc *__restrict__ seg,
     const int64_t j0 = static_cast<int64_t>(t) * kTile;
     const int64_t j1 = std::min(j0 + kTile, d.len);
     for (int64_t j = j0 + tid; j < j1; j += kThr) {
-      const float y = apply_divide(fold_scalar<Tr>(at, p, chunk_of(d.offset, j, d.chunk), j), div);
-      for (int32_t r = 0; r < p; ++r) Tr::store1(at(r), j, y);
+      const float y =
+          epi(apply_divide(fold_scalar<Tr>(at, p, chunk_of(d.offset, j, d.chunk), j), div));
+      for (int32_t r = 0; Epilogue::kStore && r < p; ++r) Tr::store1(at(r), j, y);
     }
     return;
   }
@@ -164,8 +186,8 @@ __device__ __forceinline__ void bucket_tile(const SegDesc *__restrict__ seg,
     const int64_t J = head ? k.s + lane : k.tail_begin + (lane - (V - 1));
     if (J < (head ? k.head_end : k.e)) {
       const float y =
-          apply_divide(fold_scalar<Tr>(at, p, chunk_of(d.offset, J - m, d.chunk), J), div);
-      for (int32_t r = 0; r < p; ++r) Tr::store1(at(r), J, y);
+          epi(apply_divide(fold_scalar<Tr>(at, p, chunk_of(d.offset, J - m, d.chunk), J), div));
+      for (int32_t r = 0; Epilogue::kStore && r < p; ++r) Tr::store1(at(r), J, y);
     }
   }
 
@@ -214,9 +236,14 @@ __device__ __forceinline__ void bucket_tile(const SegDesc *__restrict__ seg,
 #pragma unroll
   for (int u = 0; u < VPT; ++u) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[u][e] = apply_divide(acc[u][e], div);
+    for (int e = 0; e < V; ++e) {
+      const float v = apply_divide(acc[u][e], div);
+      // a lane past the body holds no element
+      acc[u][e] = ok[u] ? epi(v) : v;
+    }
     y[u] = Tr::narrow(acc[u]);
   }
+  if constexpr (!Epilogue::kStore) return;
   const int32_t rot = store_rotation(p, tile);
   for (int32_t r = 0; r < p; ++r) {
     void *dst = lat(ring_rank(rot, r, p));
@@ -238,8 +265,81 @@ __global__ __launch_bounds__(kBucketThreads) void bucket_allreduce_kernel(
     const void *const *__restrict__ grads, int32_t p, Divide div) {
   for (int32_t w = static_cast<int32_t>(blockIdx.x); w < n_tiles;
        w += static_cast<int32_t>(gridDim.x)) {
+    TileEpilogue<kSyncPlain, DDP_NORM_L2> epi;
     bucket_tile<Tr, VPT, RB, kNT>(seg, tile_seg, map_stride, tile_base + w, n_params, grads, p,
-                                  div);
+                                  div, epi);
+  }
+}
+
+// The same tiles with an epilogue: each workgroup (one wave) leaves its
+// tile's part of the norm in partial[tile], or scales by the coefficient.
+template <typename Tr, int VPT, int RB, bool kNT, int kMode, int NT>
+__global__ __launch_bounds__(kBucketThreads) void bucket_epilogue_kernel(
+    const SegDesc *__restrict__ seg, const int32_t *__restrict__ tile_seg, int64_t map_stride,
+    int32_t tile_base, int32_t n_tiles, int32_t n_params,
+    const void *const *__restrict__ grads, int32_t p, Divide div, double *__restrict__ partial,
+    const float *__restrict__ norm, float max_norm, float eps) {
+  static_assert(kBucketThreads == 64, "a tile's sum is joined within one wave");
+  for (int32_t w = static_cast<int32_t>(blockIdx.x); w < n_tiles;
+       w += static_cast<int32_t>(gridDim.x)) {
+    TileEpilogue<kMode, NT> epi;
+    if constexpr (kMode == kSyncScale) epi.scale = clip_coefficient(*norm, max_norm, eps);
+    bucket_tile<Tr, VPT, RB, kNT>(seg, tile_seg, map_stride, tile_base + w, n_params, grads, p,
+                                  div, epi);
+    if constexpr (kMode != kSyncScale) {
+      join_wave(epi.sum);
+      if (threadIdx.x == 0) partial[tile_base + w] = epi.sum.part();
+    }
+  }
+}
+
+// The arguments of one bucket launch, and its kernel by type, mode and norm.
+struct BucketLaunch {
+  const SegDesc *seg;
+  const int32_t *tile_seg;
+  int64_t map_stride;
+  int32_t tile0, tiles, n_params;
+  const void *const *grads;
+  int32_t p;
+  Divide div;
+  dim3 grid;
+  size_t lds;
+  hipStream_t stream;
+};
+
+template <typename Tr, int kMode, int NT>
+ddp_status launch_epilogue(const BucketLaunch &b, const SyncEpilogue &e, CallTimer &timer,
+                           bool last) {
+  return launch_lds(bucket_epilogue_kernel<Tr, kBucketVpt, kBucketRb, kBucketNt, kMode, NT>,
+                    b.grid, dim3(kBucketThreads), b.lds, b.stream, timer, last,
+                    "bucket_epilogue_kernel launch", b.seg, b.tile_seg, b.map_stride, b.tile0,
+                    b.tiles, b.n_params, b.grads, b.p, b.div, e.partial, e.norm, e.max_norm,
+                    e.eps);
+}
+
+template <typename Tr, int kMode>
+ddp_status launch_norm_type(const BucketLaunch &b, const SyncEpilogue &e, CallTimer &timer,
+                            bool last) {
+  switch (e.norm_type) {
+    case DDP_NORM_L2: return launch_epilogue<Tr, kMode, DDP_NORM_L2>(b, e, timer, last);
+    case DDP_NORM_L1: return launch_epilogue<Tr, kMode, DDP_NORM_L1>(b, e, timer, last);
+    default: return launch_epilogue<Tr, kMode, DDP_NORM_INF>(b, e, timer, last);
+  }
+}
+
+template <typename Tr>
+ddp_status launch_bucket(const BucketLaunch &b, const SyncEpilogue *e, CallTimer &timer,
+                         bool last) {
+  if (e == nullptr || e->mode == kSyncPlain) {
+    return launch_lds(bucket_allreduce_kernel<Tr, kBucketVpt, kBucketRb, kBucketNt>, b.grid,
+                      dim3(kBucketThreads), b.lds, b.stream, timer, last,
+                      "bucket_allreduce_kernel launch", b.seg, b.tile_seg, b.map_stride, b.tile0,
+                      b.tiles, b.n_params, b.grads, b.p, b.div);
+  }
+  switch (e->mode) {
+    case kSyncNorm: return launch_norm_type<Tr, kSyncNorm>(b, *e, timer, last);
+    case kFoldNorm: return launch_norm_type<Tr, kFoldNorm>(b, *e, timer, last);
+    default: return launch_epilogue<Tr, kSyncScale, DDP_NORM_L2>(b, *e, timer, last);
   }
 }
 
@@ -253,9 +353,11 @@ namespace ddpsim {
 ddp_status allreduce_buckets(const ddp_plan *plan, int32_t first_bucket, int32_t n_buckets,
                              int32_t p, void *const *d_grad_ptrs, int32_t dtype,
                              int32_t avg_mode, const int64_t *tokens, hipStream_t stream,
-                             ddp_comm_stats *stats, int32_t max_workgroups) {
+                             ddp_comm_stats *stats, int32_t max_workgroups,
+                             const SyncEpilogue *epi, CallTimer *call_timer, bool last) {
   clear_error();
-  CallTimer timer = CallTimer::take();
+  CallTimer own_timer = call_timer == nullptr ? CallTimer::take() : CallTimer();
+  CallTimer &timer = call_timer == nullptr ? own_timer : *call_timer;
   const char *what = "ddp_allreduce_buckets";
   if (plan == nullptr) return fail(DDP_EINVAL, "%s: plan is NULL", what);
   const int32_t nbk = plan_num_buckets(plan);
@@ -321,16 +423,10 @@ ddp_status allreduce_buckets(const ddp_plan *plan, int32_t first_bucket, int32_t
   // CU raised the GPT-2 p=8 launch from 5.76 to 6.05 TB/s and the Llama bf16
   // buckets by 3-4%; 6 per CU starved the channels (5.2).
   const size_t lds = residency_lds(fold_residency(DDPSIM_BUCKET_WGS_PER_CU, p));
-  if (dtype == DDP_F32) {
-    return launch_lds(bucket_allreduce_kernel<F32Traits, kBucketVpt, kBucketRb, kBucketNt>, grid,
-                      dim3(kBucketThreads), lds, stream, timer, true,
-                      "bucket_allreduce_kernel launch", seg, tile_seg, map_stride, tile0, tiles, n_params,
-                      grads, p, div);
-  }
-  return launch_lds(bucket_allreduce_kernel<BF16Traits, kBucketVpt, kBucketRb, kBucketNt>, grid,
-                    dim3(kBucketThreads), lds, stream, timer, true,
-                    "bucket_allreduce_kernel launch", seg, tile_seg, map_stride, tile0, tiles, n_params, grads,
-                    p, div);
+  const BucketLaunch launch = {seg,   tile_seg, map_stride, tile0, tiles, n_params,
+                               grads, p,        div,        grid,  lds,   stream};
+  return dtype == DDP_F32 ? launch_bucket<F32Traits>(launch, epi, timer, last)
+                          : launch_bucket<BF16Traits>(launch, epi, timer, last);
 }
 
 }  // namespace ddpsim

@@ -1,0 +1,555 @@
+// grad_norm.hip -- the global norm of each rank's gradients over many
+// tensors, and clipping by it.
+//
+// The tensors are walked through the plan's tiles of 64 vectors (1 KiB), the
+// numbering of the in-place bucket all-reduce: a wave takes a group of
+// consecutive tiles of one rank. Its lanes first fetch the group's metadata,
+// a tile per lane (descriptor index, descriptor, gradient address: three
+// dependent loads for the whole group instead of three per tensor), then the
+// wave streams the tiles with the addresses read back from those lanes.
+#include <algorithm>
+#include <cmath>
+
+#include "fold.hpp"
+#include "norm.hpp"
+
+namespace ddpsim {
+namespace {
+
+constexpr int kGroup = kNormGroup;  // tiles of a wave
+constexpr int kBatch = 8;    // tiles whose loads are in flight together
+constexpr int kWaves = 4;    // waves of a workgroup
+constexpr int kFinishThreads = 512;
+static_assert(kGroup <= 64 && kGroup % kBatch == 0, "a lane per tile");
+static_assert(kBucketThreads == 64 && kBucketVpt == 1, "a plan tile is one vector per lane");
+
+// Lane k holds tile (group * kGroup + k) of one rank.
+struct LaneTile {
+  uint64_t src;   // address of the tile's first whole vector
+  int32_t count;  // whole vectors (0..64; 0 beyond the last tile)
+  int32_t seg;    // descriptor index, -1 beyond the last tile
+  int32_t ends;   // the tile is its parameter's last
+  int32_t first;  // the tile is its parameter's first
+  // elements before and after the parameter's whole vectors (first tile only)
+  uint64_t head, tail;
+  int32_t n_head, n_tail;
+};
+
+template <typename Tr>
+__device__ __forceinline__ LaneTile lane_tile(const SegDesc *__restrict__ seg,
+                                              const int32_t *__restrict__ tile_seg,
+                                              int64_t map_stride, int64_t tile, int64_t tiles,
+                                              const void *const *__restrict__ grads, bool on) {
+  constexpr int V = Tr::kVec;
+  constexpr int64_t kElemBytes = sizeof(typename Tr::elem);
+  LaneTile x = {};
+  x.seg = -1;
+  if (!on || tile >= tiles) return x;
+  x.seg = tile_seg[tile_map_index(tile, map_stride)];
+  const SegDesc d = seg[x.seg];
+  const int64_t k = tile - d.tile_begin;
+  const uint64_t base = reinterpret_cast<uint64_t>(grads[d.param]);
+  const int64_t m = static_cast<int64_t>(base % kVecBytes) / kElemBytes;
+  const ChunkSpan c = make_span(m, d.len + m, V);  // indices from the aligned address below base
+  const uint64_t aligned = base - static_cast<uint64_t>(m * kElemBytes);
+  const int64_t left = (c.ve - c.vs) / V - k * 64;
+  x.src = aligned + static_cast<uint64_t>((c.vs / V + k * 64) * kVecBytes);
+  x.count = static_cast<int32_t>(left < 0 ? 0 : left > 64 ? 64 : left);
+  x.ends = (k + 1) * 64 * V >= d.len;
+  x.first = k == 0;
+  if (k == 0) {
+    x.head = aligned + static_cast<uint64_t>(c.s * kElemBytes);
+    x.n_head = static_cast<int32_t>(c.head_end - c.s);
+    x.tail = aligned + static_cast<uint64_t>(c.tail_begin * kElemBytes);
+    x.n_tail = static_cast<int32_t>(c.e - c.tail_begin);
+  }
+  return x;
+}
+
+__device__ __forceinline__ uint64_t read_lane(uint64_t v, int lane) {
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(v), lane);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(v >> 32), lane);
+  return (static_cast<uint64_t>(hi) << 32) | lo;
+}
+
+template <typename Tr, int NT>
+__global__ __launch_bounds__(64 * kWaves) void grad_norm_kernel(
+    const SegDesc *__restrict__ seg, const int32_t *__restrict__ tile_seg, int64_t map_stride,
+    int64_t tiles, int64_t groups, int32_t n_params, const void *const *__restrict__ ptrs,
+    double *__restrict__ partial, int64_t slots) {
+  constexpr int V = Tr::kVec;
+  const int lane = static_cast<int>(threadIdx.x) & 63;
+  const int64_t g = int64_t(blockIdx.x) * kWaves +
+                    __builtin_amdgcn_readfirstlane(static_cast<int32_t>(threadIdx.x) >> 6);
+  if (g >= groups) return;
+  const int32_t rank = static_cast<int32_t>(blockIdx.y);
+  const LaneTile mine = lane_tile<Tr>(seg, tile_seg, map_stride, g * kGroup + lane, tiles,
+                                      ptrs + static_cast<int64_t>(rank) * n_params,
+                                      lane < kGroup);
+  double *out = partial + static_cast<int64_t>(rank) * slots + g;
+  // a lane adds the odd elements at its tile's parameter's ends
+  NormSum<NT> odd;
+  for (int i = 0; i < mine.n_head; ++i) {
+    odd.add(Tr::load1(reinterpret_cast<const void *>(mine.head), i));
+  }
+  for (int i = 0; i < mine.n_tail; ++i) {
+    odd.add(Tr::load1(reinterpret_cast<const void *>(mine.tail), i));
+  }
+  int32_t cur = __builtin_amdgcn_readlane(mine.seg, 0);
+  NormSum<NT> sum;
+  auto flush = [&]() {
+    if (mine.seg == cur) sum.join(odd);
+    join_wave(sum);
+    if (lane == 0) out[cur] = sum.part();
+    sum = NormSum<NT>();
+  };
+#pragma unroll
+  for (int b = 0; b < kGroup; b += kBatch) {
+    uint4 x[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const uint64_t src = read_lane(mine.src, b + u);
+      const int32_t count = __builtin_amdgcn_readlane(mine.count, b + u);
+      x[u] = lane < count ? load_vec(reinterpret_cast<const void *>(src), lane)
+                          : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int32_t s = __builtin_amdgcn_readlane(mine.seg, b + u);
+      if (s != cur && s >= 0) {
+        flush();
+        cur = s;
+      }
+      float w[V];
+      Tr::widen(x[u], w);
+#pragma unroll
+      for (int e = 0; e < V; ++e) sum.add(w[e]);
+    }
+  }
+  flush();
+  // the group's last tile, and the slot after it if its parameter ends there
+  const int64_t left = tiles - g * kGroup;
+  const int32_t last = static_cast<int32_t>(left < kGroup ? left : kGroup) - 1;
+  if (lane == last && mine.ends) out[cur + 1] = 0.0;
+}
+
+// Block 0 joins all of a rank's partial sums into its norm; block 1 + i those
+// of descriptor i into that parameter's norm. `group` is the tiles per
+// partial sum (1: a sum per tile, without gaps).
+template <int NT>
+__global__ __launch_bounds__(kFinishThreads) void norm_finish_kernel(
+    const double *__restrict__ partial, int64_t slots, const SegDesc *__restrict__ seg,
+    int32_t group, int64_t tile_elems, int32_t n_params, float *__restrict__ norms,
+    float *__restrict__ param_norms) {
+  __shared__ double parts[kFinishThreads / 64];
+  const int32_t rank = static_cast<int32_t>(blockIdx.y);
+  int64_t i0 = 0, i1 = slots;
+  float *out = norms + rank;
+  if (blockIdx.x > 0) {
+    const int32_t s = static_cast<int32_t>(blockIdx.x) - 1;
+    const SegDesc d = seg[s];
+    const int64_t a = d.tile_begin, b = a + (d.len + tile_elems - 1) / tile_elems;
+    i0 = group == 1 ? a : a / group + s;
+    i1 = group == 1 ? b : (b - 1) / group + s + 1;
+    out = param_norms + static_cast<int64_t>(rank) * n_params + d.param;
+  }
+  const double *src = partial + static_cast<int64_t>(rank) * slots;
+  NormSum<NT> sum;
+  for (int64_t i = i0 + threadIdx.x; i < i1; i += kFinishThreads) sum.join_part(src[i]);
+  join_wave(sum);
+  if ((threadIdx.x & 63) == 0) parts[threadIdx.x >> 6] = sum.part();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    NormSum<NT> all;
+    for (int w = 0; w < kFinishThreads / 64; ++w) all.join_part(parts[w]);
+    *out = all.norm();
+  }
+}
+
+__global__ void zero_floats_kernel(float *p, int64_t n) {
+  const int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (i < n) p[i] = 0.0f;
+}
+
+// One wave per group of tiles of one rank: load, scale, store. A coefficient
+// of one changes no value, so such a rank's gradients are not touched.
+template <typename Tr>
+__global__ __launch_bounds__(64 * kWaves) void clip_kernel(
+    const SegDesc *__restrict__ seg, const int32_t *__restrict__ tile_seg, int64_t map_stride,
+    int64_t tiles, int64_t groups, int32_t n_params, const void *const *__restrict__ ptrs,
+    const float *__restrict__ norms, int32_t norm_step, float max_norm, float eps) {
+  constexpr int V = Tr::kVec;
+  const int32_t rank = static_cast<int32_t>(blockIdx.y);
+  const float c = clip_coefficient(norms[rank * norm_step], max_norm, eps);
+  if (c == 1.0f) return;
+  const int lane = static_cast<int>(threadIdx.x) & 63;
+  const int64_t g = int64_t(blockIdx.x) * kWaves +
+                    __builtin_amdgcn_readfirstlane(static_cast<int32_t>(threadIdx.x) >> 6);
+  if (g >= groups) return;
+  const LaneTile mine = lane_tile<Tr>(seg, tile_seg, map_stride, g * kGroup + lane, tiles,
+                                      ptrs + static_cast<int64_t>(rank) * n_params,
+                                      lane < kGroup);
+  for (int i = 0; i < mine.n_head; ++i) {
+    void *at = reinterpret_cast<void *>(mine.head);
+    Tr::store1(at, i, Tr::load1(at, i) * c);
+  }
+  for (int i = 0; i < mine.n_tail; ++i) {
+    void *at = reinterpret_cast<void *>(mine.tail);
+    Tr::store1(at, i, Tr::load1(at, i) * c);
+  }
+#pragma unroll
+  for (int b = 0; b < kGroup; b += kBatch) {
+    uint4 x[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const uint64_t src = read_lane(mine.src, b + u);
+      const int32_t count = __builtin_amdgcn_readlane(mine.count, b + u);
+      x[u] = lane < count ? load_vec(reinterpret_cast<const void *>(src), lane)
+                          : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const uint64_t dst = read_lane(mine.src, b + u);
+      const int32_t count = __builtin_amdgcn_readlane(mine.count, b + u);
+      float w[V];
+      Tr::widen(x[u], w);
+#pragma unroll
+      for (int e = 0; e < V; ++e) w[e] = w[e] * c;
+      if (lane < count) store_vec<false>(reinterpret_cast<void *>(dst), lane, Tr::narrow(w));
+    }
+  }
+}
+
+// Replicated gradients: a tile is read from rank 0, scaled, and written to
+// all p ranks. Ranks whose copies of a parameter sit at different offsets
+// from a 16-byte boundary take elements.
+template <typename Tr>
+__global__ __launch_bounds__(64) void clip_replicated_kernel(
+    const SegDesc *__restrict__ seg, const int32_t *__restrict__ tile_seg, int64_t map_stride,
+    int64_t tiles, int32_t n_params, const void *const *__restrict__ ptrs, int32_t p,
+    const float *__restrict__ norms, float max_norm, float eps) {
+  constexpr int V = Tr::kVec;
+  constexpr int64_t kElemBytes = sizeof(typename Tr::elem);
+  constexpr int64_t kTile = 64 * V;
+  const float c = clip_coefficient(norms[0], max_norm, eps);
+  if (c == 1.0f) return;
+  const int lane = static_cast<int>(threadIdx.x);
+  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const SegDesc d = seg[tile_seg[tile_map_index(tile, map_stride)]];
+    const int64_t t = tile - d.tile_begin;
+    const uint64_t mine =
+        lane < p ? reinterpret_cast<uint64_t>(ptrs[static_cast<int64_t>(lane) * n_params + d.param])
+                 : 0;
+    const GradPtrs at{ptrs, n_params, d.param, 0};
+    const uint64_t phase = __builtin_amdgcn_readlane(static_cast<uint32_t>(mine), 0) %
+                           static_cast<uint32_t>(kVecBytes);
+    if (!__all(lane >= p || mine % kVecBytes == phase)) {
+      for (int64_t j = t * kTile + lane; j < std::min((t + 1) * kTile, d.len); j += 64) {
+        const float y = Tr::load1(at(0), j) * c;
+        for (int32_t r = 0; r < p; ++r) Tr::store1(at(r), j, y);
+      }
+      continue;
+    }
+    const int64_t m = static_cast<int64_t>(phase) / kElemBytes;
+    const GradPtrs base{ptrs, n_params, d.param, m * kElemBytes};
+    const LanePtrs lat{mine - static_cast<uint64_t>(m * kElemBytes)};
+    const ChunkSpan k = make_span(m, d.len + m, V);
+    if (t == 0 && lane >= 64 - 2 * (V - 1)) {
+      const int i = lane - (64 - 2 * (V - 1));
+      const bool head = i < V - 1;
+      const int64_t J = head ? k.s + i : k.tail_begin + (i - (V - 1));
+      if (J < (head ? k.head_end : k.e)) {
+        const float y = Tr::load1(base(0), J) * c;
+        for (int32_t r = 0; r < p; ++r) Tr::store1(base(r), J, y);
+      }
+    }
+    const int64_t v = k.vs / V + t * 64 + lane;
+    const bool ok = v < k.ve / V;
+    const int32_t rot = store_rotation(p, static_cast<uint32_t>(tile));
+    float w[V];
+    Tr::widen(ok ? load_vec(lat(0), v) : make_uint4(0, 0, 0, 0), w);
+#pragma unroll
+    for (int e = 0; e < V; ++e) w[e] = w[e] * c;
+    const uint4 y = Tr::narrow(w);
+    for (int32_t r = 0; r < p; ++r) {
+      void *dst = lat(ring_rank(rot, r, p));
+      if (ok) store_vec<false>(dst, v, y);
+    }
+  }
+}
+
+// Plan, rank count, type and table of a norm or clip call.
+ddp_status check_call(const char *what, const ddp_plan *plan, int32_t p, const void *d_grad_ptrs,
+                      int32_t dtype, PlanTiles *t) {
+  if (!plan_tiles(plan, t)) return fail(DDP_EINVAL, "%s: plan is NULL", what);
+  ddp_status s = check_p(p, what);
+  if (s != DDP_OK) return s;
+  const int eb = elem_bytes_of(dtype);
+  if (eb == 0) return fail(DDP_EINVAL, "%s: unknown dtype %d", what, dtype);
+  if (eb != t->elem_bytes) {
+    return fail(DDP_EINVAL, "%s: dtype has %d-byte elements, the plan %d", what, eb,
+                t->elem_bytes);
+  }
+  if (t->seg_p == 0) {
+    return fail(DDP_ENOTREADY, "%s: call ddp_plan_upload_segments first", what);
+  }
+  if (t->tiles > 0 && d_grad_ptrs == nullptr) {
+    return fail(DDP_EINVAL, "%s: gradient pointer table is NULL", what);
+  }
+  return DDP_OK;
+}
+
+ddp_status check_norm_type(const char *what, int32_t norm_type) {
+  if (norm_type != DDP_NORM_L2 && norm_type != DDP_NORM_L1 && norm_type != DDP_NORM_INF) {
+    return fail(DDP_EINVAL, "%s: unknown norm type %d", what, norm_type);
+  }
+  return DDP_OK;
+}
+
+ddp_status check_bound(const char *what, float max_norm, float eps) {
+  if (!(max_norm >= 0.0f)) return fail(DDP_EINVAL, "%s: max_norm must be >= 0", what);
+  if (!(eps >= 0.0f) || std::isinf(eps)) {
+    return fail(DDP_EINVAL, "%s: eps must be finite and >= 0", what);
+  }
+  return DDP_OK;
+}
+
+ddp_status check_out(const char *what, const float *d_norms, const float *d_param_norms) {
+  if (d_norms == nullptr) return fail(DDP_EINVAL, "%s: d_norms is NULL", what);
+  if (reinterpret_cast<uintptr_t>(d_norms) % 4 != 0 ||
+      reinterpret_cast<uintptr_t>(d_param_norms) % 4 != 0) {
+    return fail(DDP_EALIGN, "%s: the norms are not 4-byte aligned", what);
+  }
+  return DDP_OK;
+}
+
+ddp_status check_scratch(const char *what, const void *workspace, size_t bytes, size_t need) {
+  return check_workspace(what, workspace, bytes, need, nullptr, 0, 0);
+}
+
+template <int NT>
+ddp_status launch_finish_nt(const PlanTiles &t, const double *partial, int64_t slots,
+                            int32_t group, int32_t ranks, float *d_norms, float *d_param_norms,
+                            hipStream_t stream, CallTimer &timer, bool last) {
+  if (d_param_norms != nullptr && t.nseg < t.n_params) {
+    // parameters without elements have no descriptor
+    const int64_t n = static_cast<int64_t>(ranks) * t.n_params;
+    ddp_status s = launch(zero_floats_kernel, dim3(static_cast<uint32_t>(ceil_div(n, 256))),
+                          dim3(256), stream, timer, false, "zero_floats_kernel launch",
+                          d_param_norms, n);
+    if (s != DDP_OK) return s;
+  }
+  const uint32_t blocks = 1 + (d_param_norms != nullptr ? static_cast<uint32_t>(t.nseg) : 0);
+  return launch(norm_finish_kernel<NT>, dim3(blocks, static_cast<uint32_t>(ranks)),
+                dim3(kFinishThreads), stream, timer, last, "norm_finish_kernel launch", partial,
+                slots, t.seg, group, bucket_tile_elems(kVecBytes / t.elem_bytes), t.n_params,
+                d_norms, d_param_norms);
+}
+
+ddp_status launch_finish(const PlanTiles &t, int32_t norm_type, const double *partial,
+                         int64_t slots, int32_t group, int32_t ranks, float *d_norms,
+                         float *d_param_norms, hipStream_t stream, CallTimer &timer, bool last) {
+  switch (norm_type) {
+    case DDP_NORM_L2:
+      return launch_finish_nt<DDP_NORM_L2>(t, partial, slots, group, ranks, d_norms,
+                                           d_param_norms, stream, timer, last);
+    case DDP_NORM_L1:
+      return launch_finish_nt<DDP_NORM_L1>(t, partial, slots, group, ranks, d_norms,
+                                           d_param_norms, stream, timer, last);
+    default:
+      return launch_finish_nt<DDP_NORM_INF>(t, partial, slots, group, ranks, d_norms,
+                                            d_param_norms, stream, timer, last);
+  }
+}
+
+template <typename Tr, int NT>
+ddp_status launch_norm(const PlanTiles &t, int32_t p, const void *const *ptrs, double *partial,
+                       int64_t slots, hipStream_t stream, CallTimer &timer) {
+  const int64_t groups = norm_groups(t);
+  return launch(grad_norm_kernel<Tr, NT>,
+                dim3(static_cast<uint32_t>(ceil_div(groups, kWaves)), static_cast<uint32_t>(p)),
+                dim3(64 * kWaves), stream, timer, false, "grad_norm_kernel launch", t.seg,
+                t.tile_seg, t.map_stride, t.tiles, groups, t.n_params, ptrs, partial, slots);
+}
+
+template <typename Tr>
+ddp_status launch_norm_type(int32_t norm_type, const PlanTiles &t, int32_t p,
+                            const void *const *ptrs, double *partial, int64_t slots,
+                            hipStream_t stream, CallTimer &timer) {
+  switch (norm_type) {
+    case DDP_NORM_L2:
+      return launch_norm<Tr, DDP_NORM_L2>(t, p, ptrs, partial, slots, stream, timer);
+    case DDP_NORM_L1:
+      return launch_norm<Tr, DDP_NORM_L1>(t, p, ptrs, partial, slots, stream, timer);
+    default:
+      return launch_norm<Tr, DDP_NORM_INF>(t, p, ptrs, partial, slots, stream, timer);
+  }
+}
+
+template <typename Tr>
+ddp_status launch_clip(const PlanTiles &t, int32_t p, const void *const *ptrs,
+                       const float *d_norms, int32_t n_norms, float max_norm, float eps,
+                       bool replicated, hipStream_t stream, CallTimer &timer) {
+  if (replicated) {
+    const int64_t blocks = std::min(t.tiles, int64_t(UINT32_MAX) / 64);
+    return launch(clip_replicated_kernel<Tr>, dim3(static_cast<uint32_t>(blocks)), dim3(64),
+                  stream, timer, true, "clip_replicated_kernel launch", t.seg, t.tile_seg,
+                  t.map_stride, t.tiles, t.n_params, ptrs, p, d_norms, max_norm, eps);
+  }
+  const int64_t groups = norm_groups(t);
+  return launch(clip_kernel<Tr>,
+                dim3(static_cast<uint32_t>(ceil_div(groups, kWaves)), static_cast<uint32_t>(p)),
+                dim3(64 * kWaves), stream, timer, true, "clip_kernel launch", t.seg, t.tile_seg,
+                t.map_stride, t.tiles, groups, t.n_params, ptrs, d_norms,
+                n_norms == 1 ? 0 : 1, max_norm, eps);
+}
+
+}  // namespace
+}  // namespace ddpsim
+
+using namespace ddpsim;
+
+extern "C" ddp_status ddp_grad_norm(const ddp_plan *plan, int32_t p,
+                                    const void *const *d_grad_ptrs, int32_t dtype,
+                                    int32_t norm_type, float *d_norms, float *d_param_norms,
+                                    void *workspace, size_t workspace_bytes,
+                                    hipStream_t stream) {
+  clear_error();
+  CallTimer timer = CallTimer::take();
+  const char *what = "ddp_grad_norm";
+  PlanTiles t;
+  ddp_status s = check_call(what, plan, p, d_grad_ptrs, dtype, &t);
+  if (s == DDP_OK) s = check_norm_type(what, norm_type);
+  if (s == DDP_OK) s = check_out(what, d_norms, d_param_norms);
+  if (s == DDP_OK) {
+    s = check_scratch(what, workspace, workspace_bytes, ddp_grad_norm_workspace(plan, p));
+  }
+  if (s != DDP_OK) return s;
+  double *partial = static_cast<double *>(workspace);
+  const int64_t slots = norm_slots(t);
+  if (t.tiles > 0) {
+    s = dtype == DDP_F32
+            ? launch_norm_type<F32Traits>(norm_type, t, p, d_grad_ptrs, partial, slots, stream,
+                                          timer)
+            : launch_norm_type<BF16Traits>(norm_type, t, p, d_grad_ptrs, partial, slots, stream,
+                                           timer);
+    if (s != DDP_OK) return s;
+  }
+  return launch_finish(t, norm_type, partial, slots, kGroup, p, d_norms, d_param_norms, stream,
+                       timer, true);
+}
+
+extern "C" ddp_status ddp_clip_grads(const ddp_plan *plan, int32_t p, void *const *d_grad_ptrs,
+                                     int32_t dtype, const float *d_norms, int32_t n_norms,
+                                     float max_norm, float eps, int32_t replicated,
+                                     hipStream_t stream) {
+  clear_error();
+  CallTimer timer = CallTimer::take();
+  const char *what = "ddp_clip_grads";
+  PlanTiles t;
+  ddp_status s = check_call(what, plan, p, d_grad_ptrs, dtype, &t);
+  if (s == DDP_OK) s = check_out(what, d_norms, nullptr);
+  if (s == DDP_OK) s = check_bound(what, max_norm, eps);
+  if (s != DDP_OK) return s;
+  if (replicated != 0 && replicated != 1) {
+    return fail(DDP_EINVAL, "%s: replicated must be 0 or 1", what);
+  }
+  if (n_norms != 1 && (n_norms != p || replicated)) {
+    return fail(DDP_EINVAL, "%s: n_norms=%d: one norm%s", what, n_norms,
+                replicated ? " for replicated gradients" : ", or one per rank");
+  }
+  if (t.tiles == 0) return DDP_OK;
+  if (dtype == DDP_F32) {
+    return launch_clip<F32Traits>(t, p, d_grad_ptrs, d_norms, n_norms, max_norm, eps,
+                                  replicated != 0, stream, timer);
+  }
+  return launch_clip<BF16Traits>(t, p, d_grad_ptrs, d_norms, n_norms, max_norm, eps,
+                                 replicated != 0, stream, timer);
+}
+
+extern "C" ddp_status ddp_allreduce_buckets_norm(const ddp_plan *plan, int32_t first_bucket,
+                                                 int32_t n_buckets, int32_t p,
+                                                 void *const *d_grad_ptrs, int32_t dtype,
+                                                 int32_t avg_mode, const int64_t *tokens,
+                                                 int32_t norm_type, void *workspace,
+                                                 size_t workspace_bytes, hipStream_t stream,
+                                                 ddp_comm_stats *stats) {
+  clear_error();
+  CallTimer timer = CallTimer::take();
+  const char *what = "ddp_allreduce_buckets_norm";
+  ddp_status s = check_norm_type(what, norm_type);
+  if (s == DDP_OK) {
+    s = check_scratch(what, workspace, workspace_bytes, ddp_sync_norm_workspace(plan));
+  }
+  if (s != DDP_OK) return s;
+  const SyncEpilogue epi = {kSyncNorm, norm_type, static_cast<double *>(workspace), nullptr, 0, 0};
+  return allreduce_buckets(plan, first_bucket, n_buckets, p, d_grad_ptrs, dtype, avg_mode, tokens,
+                           stream, stats, DDPSIM_BUCKET_MAX_WORKGROUPS, &epi, &timer);
+}
+
+extern "C" ddp_status ddp_grad_norm_finish(const ddp_plan *plan, int32_t norm_type,
+                                           float *d_norm, float *d_param_norms, void *workspace,
+                                           size_t workspace_bytes, hipStream_t stream) {
+  clear_error();
+  CallTimer timer = CallTimer::take();
+  const char *what = "ddp_grad_norm_finish";
+  PlanTiles t;
+  if (!plan_tiles(plan, &t)) return fail(DDP_EINVAL, "%s: plan is NULL", what);
+  if (t.seg_p == 0) {
+    return fail(DDP_ENOTREADY, "%s: call ddp_plan_upload_segments first", what);
+  }
+  ddp_status s = check_norm_type(what, norm_type);
+  if (s == DDP_OK) s = check_out(what, d_norm, d_param_norms);
+  if (s == DDP_OK) {
+    s = check_scratch(what, workspace, workspace_bytes, ddp_sync_norm_workspace(plan));
+  }
+  if (s != DDP_OK) return s;
+  return launch_finish(t, norm_type, static_cast<double *>(workspace), t.tiles, 1, 1, d_norm,
+                       d_param_norms, stream, timer, true);
+}
+
+extern "C" ddp_status ddp_allreduce_clip(const ddp_plan *plan, int32_t p,
+                                         void *const *d_grad_ptrs, int32_t dtype,
+                                         int32_t avg_mode, const int64_t *tokens,
+                                         int32_t norm_type, float max_norm, float eps,
+                                         float *d_norm, float *d_param_norms, void *workspace,
+                                         size_t workspace_bytes, hipStream_t stream,
+                                         ddp_comm_stats *stats) {
+  clear_error();
+  CallTimer timer = CallTimer::take();
+  const char *what = "ddp_allreduce_clip";
+  PlanTiles t;
+  ddp_status s = check_call(what, plan, p, d_grad_ptrs, dtype, &t);
+  if (s == DDP_OK) s = check_norm_type(what, norm_type);
+  if (s == DDP_OK) s = check_bound(what, max_norm, eps);
+  if (s == DDP_OK) s = check_out(what, d_norm, d_param_norms);
+  if (s == DDP_OK) {
+    s = check_scratch(what, workspace, workspace_bytes, ddp_sync_norm_workspace(plan));
+  }
+  if (s != DDP_OK) return s;
+  if (t.seg_p != p) {
+    return fail(DDP_ENOTREADY, "%s: call ddp_plan_upload_segments with p=%d first", what, p);
+  }
+  Divide div;
+  s = make_divide(avg_mode, p, tokens, &div);
+  if (s != DDP_OK) return s;
+  SyncEpilogue epi = {kFoldNorm, norm_type, static_cast<double *>(workspace), d_norm, max_norm, eps};
+  const int32_t nb = ddp_plan_num_buckets(plan);
+  if (stats != nullptr) *stats = ddp_comm_stats{};
+  if (nb > 0) {
+    s = allreduce_buckets(plan, 0, nb, p, d_grad_ptrs, dtype, avg_mode, tokens, stream, nullptr,
+                          DDPSIM_BUCKET_MAX_WORKGROUPS, &epi, &timer, false);
+    if (s != DDP_OK) return s;
+  }
+  s = launch_finish(t, norm_type, epi.partial, t.tiles, 1, 1, d_norm, d_param_norms, stream,
+                    timer, t.tiles == 0);
+  if (s != DDP_OK || nb == 0) return s;
+  epi.mode = kSyncScale;
+  s = allreduce_buckets(plan, 0, nb, p, d_grad_ptrs, dtype, avg_mode, tokens, stream, stats,
+                        DDPSIM_BUCKET_MAX_WORKGROUPS, &epi, &timer, true);
+  // the gradients are folded twice: once for the norm, once for the result
+  if (s == DDP_OK && stats != nullptr) {
+    stats->hbm_bytes = 3 * int64_t(p) * t.elems * t.elem_bytes;
+  }
+  return s;
+}

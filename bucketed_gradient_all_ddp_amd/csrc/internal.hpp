@@ -14,6 +14,8 @@
 
 namespace ddpsim {
 
+struct CallTimer;
+
 constexpr int kThreads = 256;               // threads per workgroup (4 waves)
 constexpr int kMaxRanks = DDP_MAX_RANKS;
 constexpr int kVecBytes = 16;               // one global_load/store_dwordx4
@@ -166,12 +168,57 @@ constexpr int32_t kMaxFanoutWaves = 8;
 // smallest power of two W (at most kMaxFanoutWaves) with W * 4 >= dests.
 int32_t fanout_waves(int32_t dests);
 
+// What the norm and clip kernels need of a plan (defined in plan.cpp): the
+// tiles and descriptors of all its buckets, and the device table that
+// ddp_plan_upload_segments filled (its tiles and parameters are the same for
+// every p; seg_p is 0 when there is none).
+struct PlanTiles {
+  const SegDesc *seg;
+  const int32_t *tile_seg;
+  int64_t map_stride;
+  int64_t tiles;
+  int64_t elems;
+  int32_t nseg;  // parameters with elements
+  int32_t n_params;
+  int32_t elem_bytes;
+  int32_t seg_p;
+};
+bool plan_tiles(const ddp_plan *plan, PlanTiles *out);
+
+// ddp_grad_norm: a wave takes kNormGroup consecutive tiles of a rank and
+// writes one partial sum per parameter it touches, at slot (group +
+// descriptor index): consecutive in tile order. Where a parameter ends with
+// its group the next used slot is one further on; the group fills the slot
+// between with a zero, so that all norm_slots values of a rank can be joined.
+constexpr int kNormGroup = 16;
+int64_t norm_groups(const PlanTiles &t);
+int64_t norm_slots(const PlanTiles &t);
+
+// What a bucket launch does with the averaged values besides storing them.
+//   kSyncPlain   the all-reduce alone
+//   kSyncNorm    the all-reduce, and each tile's part of the norm to `partial`
+//   kFoldNorm    each tile's part of the norm only; the gradients stay
+//   kSyncScale   the all-reduce of the average times the clip coefficient of
+//                *norm
+enum SyncMode : int32_t { kSyncPlain = 0, kSyncNorm = 1, kFoldNorm = 2, kSyncScale = 3 };
+struct SyncEpilogue {
+  int32_t mode;
+  int32_t norm_type;
+  double *partial;    // one value per plan tile
+  const float *norm;  // device
+  float max_norm, eps;
+};
+
 // ddp_allreduce_buckets with an optional cap on its workgroups (0: one per
-// tile). Defined in bucket_allreduce.hip; the reducer uses the cap.
+// tile) and an epilogue (nullptr: none). Defined in bucket_allreduce.hip; the
+// reducer uses the cap. `timer` is the call's (nullptr: taken here), `last`
+// whether its last launch is this one.
 ddp_status allreduce_buckets(const ddp_plan *plan, int32_t first_bucket, int32_t n_buckets,
                              int32_t p, void *const *d_grad_ptrs, int32_t dtype,
                              int32_t avg_mode, const int64_t *tokens, hipStream_t stream,
-                             ddp_comm_stats *stats, int32_t max_workgroups);
+                             ddp_comm_stats *stats, int32_t max_workgroups,
+                             const SyncEpilogue *epi = nullptr, CallTimer *timer = nullptr,
+                             bool last = true);
 
 // p, n, dtype, averaging and rank buffers of an in-place all-reduce.
 ddp_status validate_allreduce(void *const *bufs, int32_t p, int64_t n, int32_t dtype,

@@ -110,6 +110,29 @@ bool plan_segment_info(const ddp_plan *plan, int32_t b, int32_t *first, int32_t 
   return true;
 }
 
+bool plan_tiles(const ddp_plan *plan, PlanTiles *out) {
+  std::memset(out, 0, sizeof *out);
+  if (plan == nullptr) return false;
+  out->n_params = plan->n_params;
+  out->elem_bytes = plan->elem_bytes;
+  out->seg_p = plan->seg_p;
+  const int64_t tile_elems = bucket_tile_elems(kVecBytes / plan->elem_bytes);
+  for (int64_t n : plan->numel) {
+    if (n == 0) continue;
+    ++out->nseg;
+    out->tiles += ceil_div(n, tile_elems);
+    out->elems += n;
+  }
+  if (plan->seg_p != 0) {
+    out->seg = static_cast<const SegDesc *>(plan->d_seg);
+    out->tile_seg = plan_tile_map(plan, &out->map_stride);
+  }
+  return true;
+}
+
+int64_t norm_groups(const PlanTiles &t) { return ceil_div(t.tiles, kNormGroup); }
+int64_t norm_slots(const PlanTiles &t) { return norm_groups(t) + t.nseg; }
+
 // One descriptor per parameter with elements, bucket after bucket, carrying
 // its offset in the bucket's flat index space and the bucket's ring chunk
 // size ceil(n_b / p); each parameter is cut into tiles of bucket_tile_elems
@@ -155,6 +178,18 @@ static bool build_segments(const ddp_plan *plan, int32_t p, std::vector<SegDesc>
 // Entries of the tile map as stored (grouped by tile mod kXcds, each group
 // padded to the same length).
 static int64_t map_stride(size_t tiles) { return ceil_div(static_cast<int64_t>(tiles), kXcds); }
+
+extern "C" size_t ddp_grad_norm_workspace(const ddp_plan *plan, int32_t p) {
+  PlanTiles t;
+  if (!plan_tiles(plan, &t) || p < 1 || p > kMaxRanks) return 0;
+  return sizeof(double) * static_cast<size_t>(p) * static_cast<size_t>(norm_slots(t));
+}
+
+extern "C" size_t ddp_sync_norm_workspace(const ddp_plan *plan) {
+  PlanTiles t;
+  if (!plan_tiles(plan, &t)) return 0;
+  return sizeof(double) * static_cast<size_t>(t.tiles);
+}
 
 extern "C" size_t ddp_plan_segment_bytes(const ddp_plan *plan, int32_t p) {
   if (plan == nullptr || p < 1 || p > kMaxRanks) return 0;

@@ -51,6 +51,7 @@ struct ddp_reducer {
   int32_t next = 0;
   int32_t marks = 0;
   int32_t max_workgroups = 0;  // cap on each launch's workgroups (0: none)
+  SyncEpilogue norm = {};      // the norm's partial sums, if asked for
   bool active = false;
   std::vector<int32_t> log_mark, log_first, log_count;
   std::vector<int32_t> ready_order;  // parameters in the order marked, this pass
@@ -128,6 +129,26 @@ extern "C" ddp_status ddp_reducer_set_max_workgroups(ddp_reducer *r, int32_t max
   return DDP_OK;
 }
 
+extern "C" ddp_status ddp_reducer_set_norm(ddp_reducer *r, int32_t norm_type, void *workspace,
+                                           size_t workspace_bytes) {
+  clear_error();
+  const char *what = "ddp_reducer_set_norm";
+  if (r == nullptr) return fail(DDP_EINVAL, "%s: reducer is NULL", what);
+  if (r->active) return fail(DDP_EINVAL, "%s: a backward pass is in progress", what);
+  if (workspace == nullptr) {
+    r->norm = SyncEpilogue{};
+    return DDP_OK;
+  }
+  if (norm_type != DDP_NORM_L2 && norm_type != DDP_NORM_L1 && norm_type != DDP_NORM_INF) {
+    return fail(DDP_EINVAL, "%s: unknown norm type %d", what, norm_type);
+  }
+  ddp_status s = check_workspace(what, workspace, workspace_bytes,
+                                 ddp_sync_norm_workspace(r->plan), nullptr, 0, 0);
+  if (s != DDP_OK) return s;
+  r->norm = SyncEpilogue{kSyncNorm, norm_type, static_cast<double *>(workspace), nullptr, 0, 0};
+  return DDP_OK;
+}
+
 extern "C" ddp_status ddp_reducer_prepare(ddp_reducer *r) {
   clear_error();
   if (r == nullptr) return fail(DDP_EINVAL, "ddp_reducer_prepare: reducer is NULL");
@@ -192,7 +213,8 @@ extern "C" ddp_status ddp_reducer_mark_ready(ddp_reducer *r, int32_t param,
   if (s == DDP_OK) {
     s = allreduce_buckets(r->plan, r->next, end - r->next, r->p, r->grads, r->dtype,
                           r->avg_mode, r->tokens.empty() ? nullptr : r->tokens.data(), r->comm,
-                          nullptr, r->max_workgroups);
+                          nullptr, r->max_workgroups,
+                          r->norm.mode == kSyncNorm ? &r->norm : nullptr);
   }
   if (s != DDP_OK) {
     r->failed = s;

@@ -4,9 +4,10 @@
  * averaging, unflatten, the in-place bucket all-reduce and the reducer that
  * launches it as gradients become ready, the standalone reduce-scatter /
  * all-gather / broadcast, the logarithmic-latency all-reduce schedules and
- * their choice by size, the overlapped step-time model, and the coalesced
- * broadcast of parameters and buffers), with p simulated ranks whose
- * buffers all live in the HBM of one gfx950 GPU.
+ * their choice by size, the overlapped step-time model, the coalesced
+ * broadcast of parameters and buffers, and the norm and clipping of the
+ * gradients), with p simulated ranks whose buffers all live in the HBM of
+ * one gfx950 GPU.
  *
  * Pages this interface follows, cited by title and section:
  *   [DDP] "PyTorch DDP Deep Dive -- Initialization, Buffer Broadcast, the
@@ -307,6 +308,112 @@ ddp_status ddp_allreduce_buckets(const ddp_plan *plan, int32_t first_bucket,
                                  hipStream_t stream, ddp_comm_stats *stats);
 
 /* ----------------------------------------------------------------------- */
+/* Gradient norm and clipping                                              */
+/* ----------------------------------------------------------------------- */
+
+/* The norm of a set of gradients taken as one vector over all parameters:
+ * the square root of the sum of squares, the sum of magnitudes, or the
+ * largest magnitude. Sums are held in 64 bits from the first element on and
+ * rounded to fp32 once, so a norm that fits fp32 neither overflows nor
+ * vanishes on the way; the order of the additions is fixed, so equal inputs
+ * give equal bits. A NaN among the gradients makes the norm NaN; otherwise an
+ * infinity makes it infinite. The norm of no elements is 0. */
+typedef enum { DDP_NORM_L2 = 0, DDP_NORM_L1 = 1, DDP_NORM_INF = 2 } ddp_norm_type;
+
+/* Workspace bytes ddp_grad_norm needs for p ranks (0 for bad arguments). */
+size_t ddp_grad_norm_workspace(const ddp_plan *plan, int32_t p);
+
+/* The norm of each of p ranks' gradients, over all parameters of the plan,
+ * read once. The plan needs the descriptor table of
+ * ddp_plan_upload_segments, uploaded for any number of ranks.
+ *   d_grad_ptrs    DEVICE array of p * n_params addresses, rank-major, each
+ *                  aligned to its element size (pass d_grad_ptrs + r *
+ *                  n_params with p = 1 for rank r alone)
+ *   d_norms        DEVICE array of p floats: rank r's norm
+ *   d_param_norms  DEVICE array of p * n_params floats (rank-major), or NULL:
+ *                  the norm of each gradient by itself (0 for a parameter
+ *                  without elements)
+ *   workspace      ddp_grad_norm_workspace(plan, p) bytes, 16-byte aligned;
+ *                  written before it is read; calls that may overlap in time
+ *                  need workspaces of their own
+ * Errors: DDP_EINVAL, DDP_ERANGE (p), DDP_ENOTREADY (no descriptor table),
+ * DDP_EALIGN, DDP_EWORKSPACE. */
+ddp_status ddp_grad_norm(const ddp_plan *plan, int32_t p,
+                         const void *const *d_grad_ptrs, int32_t dtype,
+                         int32_t norm_type, float *d_norms,
+                         float *d_param_norms, void *workspace,
+                         size_t workspace_bytes, hipStream_t stream);
+
+/* Clip p ranks' gradients in place: every element times
+ *     c = min(1, max_norm / (norm + eps))
+ * (one correctly rounded fp32 division; the product in fp32, rounded to the
+ * gradients' type). The norm comes from device memory, so no host
+ * synchronisation stands between the norm and the clip.
+ *   d_norms     DEVICE array of n_norms floats: one norm for every rank, or
+ *               (n_norms = p) rank r's own
+ *   max_norm    >= 0; infinity: no clipping
+ *   eps         >= 0, finite (usually 1e-6)
+ *   replicated  1: every rank holds rank 0's gradients (as after an
+ *               all-reduce); they are read from rank 0 and written to all
+ *               ranks, (1 + p) bytes-per-element instead of 2 p. Needs
+ *               n_norms = 1. 0: each rank's gradients are its own.
+ * Gradients whose coefficient is 1 are not written. A norm of 0 and an
+ * infinite max_norm make c = 1, an infinite norm c = 0, a NaN norm c = NaN.
+ * Errors: as ddp_grad_norm, without the workspace's. Gradients must not
+ * overlap (as ddp_allreduce_bucket). */
+ddp_status ddp_clip_grads(const ddp_plan *plan, int32_t p,
+                          void *const *d_grad_ptrs, int32_t dtype,
+                          const float *d_norms, int32_t n_norms,
+                          float max_norm, float eps, int32_t replicated,
+                          hipStream_t stream);
+
+/* Workspace bytes of the three entry points below (0 for a NULL plan). */
+size_t ddp_sync_norm_workspace(const ddp_plan *plan);
+
+/* ddp_allreduce_buckets, and in the same pass the norm's partial sums of the
+ * averaged gradients of those buckets, left in `workspace` (16-byte aligned,
+ * ddp_sync_norm_workspace(plan) bytes, each bucket's sums at a place of
+ * their own). The gradients end with the bits of ddp_allreduce_buckets; the
+ * norm is that of the fp32 averages, before bf16 rounds them. Once every
+ * bucket of the plan has been through it (in one run or several, on any
+ * streams ordered before the call), ddp_grad_norm_finish joins the sums with
+ * the same norm_type. Errors: as ddp_allreduce_buckets, plus DDP_EWORKSPACE
+ * and DDP_EALIGN for the workspace. */
+ddp_status ddp_allreduce_buckets_norm(const ddp_plan *plan,
+                                      int32_t first_bucket, int32_t n_buckets,
+                                      int32_t p, void *const *d_grad_ptrs,
+                                      int32_t dtype, int32_t avg_mode,
+                                      const int64_t *tokens, int32_t norm_type,
+                                      void *workspace, size_t workspace_bytes,
+                                      hipStream_t stream,
+                                      ddp_comm_stats *stats);
+
+/* Join the partial sums that ddp_allreduce_buckets_norm left for every
+ * bucket of the plan: *d_norm receives the norm, d_param_norms (n_params
+ * floats, or NULL) each parameter's. Errors: as ddp_grad_norm. */
+ddp_status ddp_grad_norm_finish(const ddp_plan *plan, int32_t norm_type,
+                                float *d_norm, float *d_param_norms,
+                                void *workspace, size_t workspace_bytes,
+                                hipStream_t stream);
+
+/* The all-reduce of every bucket, the norm of the averaged gradient and the
+ * clip as one call: afterwards every rank's gradients hold c times the fp32
+ * average (c as in ddp_clip_grads), rounded once to the gradients' type, and
+ * *d_norm (and d_param_norms, if not NULL) the norm before clipping. In fp32
+ * these are the bits of ddp_allreduce_buckets_norm, ddp_grad_norm_finish and
+ * ddp_clip_grads one after another; in bf16 those round twice. The
+ * descriptor table must be the one for p. The stats describe the ring
+ * schedules, with the device traffic of this call. Errors: as
+ * ddp_allreduce_buckets_norm and ddp_clip_grads. */
+ddp_status ddp_allreduce_clip(const ddp_plan *plan, int32_t p,
+                              void *const *d_grad_ptrs, int32_t dtype,
+                              int32_t avg_mode, const int64_t *tokens,
+                              int32_t norm_type, float max_norm, float eps,
+                              float *d_norm, float *d_param_norms,
+                              void *workspace, size_t workspace_bytes,
+                              hipStream_t stream, ddp_comm_stats *stats);
+
+/* ----------------------------------------------------------------------- */
 /* Reducer: bucket all-reduces launched as gradients become ready           */
 /* ----------------------------------------------------------------------- */
 
@@ -366,6 +473,15 @@ int32_t ddp_reducer_launch_log(const ddp_reducer *reducer, int32_t *at_mark,
  * Errors: DDP_EINVAL for a NULL reducer or a negative cap. */
 ddp_status ddp_reducer_set_max_workgroups(ddp_reducer *reducer,
                                           int32_t max_workgroups);
+/* Have every all-reduce launch of the reducer also leave the norm's partial
+ * sums of its buckets in `workspace`, as ddp_allreduce_buckets_norm does;
+ * after a finalize, ddp_grad_norm_finish on a stream ordered after it joins
+ * them, and ddp_clip_grads (replicated) clips. workspace: DEVICE memory of
+ * ddp_sync_norm_workspace(plan) bytes, kept alive while the reducer runs;
+ * NULL: no norm (the default). Errors: DDP_EINVAL (NULL reducer, during a
+ * pass, unknown norm type), DDP_EWORKSPACE, DDP_EALIGN. */
+ddp_status ddp_reducer_set_norm(ddp_reducer *reducer, int32_t norm_type,
+                                void *workspace, size_t workspace_bytes);
 /* The parameters in the order they were marked ready in the current or last
  * pass (writes at most `capacity`; returns the count, -1 for NULL): the
  * order from which ddp_bucket_plan_ordered rebuilds the buckets. */
