@@ -422,7 +422,12 @@ ddp_status allreduce_buckets(const ddp_plan *plan, int32_t first_bucket, int32_t
   // every HBM channel than it keeps rows open. Bounding residency at 11 per
   // CU raised the GPT-2 p=8 launch from 5.76 to 6.05 TB/s and the Llama bf16
   // buckets by 3-4%; 6 per CU starved the channels (5.2).
-  const size_t lds = residency_lds(fold_residency(DDPSIM_BUCKET_WGS_PER_CU, p));
+  // A fold that stores nothing has p streams per workgroup: bounded at 11 it
+  // read the 8 ranks' GPT-2 gradients at 5.3 TB/s, at 14, 18 and 24 per CU at
+  // 6.5, 6.9 and 6.8 (Llama layers in bf16 4.7, and 5.9, 6.3, 6.3).
+  const bool reads = epi != nullptr && epi->mode == kFoldNorm;
+  const size_t lds = residency_lds(
+      fold_residency(reads ? DDPSIM_FOLD_WGS_PER_CU : DDPSIM_BUCKET_WGS_PER_CU, p));
   const BucketLaunch launch = {seg,   tile_seg, map_stride, tile0, tiles, n_params,
                                grads, p,        div,        grid,  lds,   stream};
   return dtype == DDP_F32 ? launch_bucket<F32Traits>(launch, epi, timer, last)

@@ -19,7 +19,9 @@ namespace {
 constexpr int kGroup = kNormGroup;  // tiles of a wave
 constexpr int kBatch = 8;    // tiles whose loads are in flight together
 constexpr int kWaves = 4;    // waves of a workgroup
-constexpr int kFinishThreads = 512;
+constexpr int kFinishWaves = 16;     // waves of a block of the last join
+constexpr int64_t kWaveSlots = 512;  // sums of a parameter that one wave joins
+constexpr int kJoinGroup = kNormJoinGroup;
 static_assert(kGroup <= 64 && kGroup % kBatch == 0, "a lane per tile");
 static_assert(kBucketThreads == 64 && kBucketVpt == 1, "a plan tile is one vector per lane");
 
@@ -133,36 +135,111 @@ __global__ __launch_bounds__(64 * kWaves) void grad_norm_kernel(
   if (lane == last && mine.ends) out[cur + 1] = 0.0;
 }
 
-// Block 0 joins all of a rank's partial sums into its norm; block 1 + i those
-// of descriptor i into that parameter's norm. `group` is the tiles per
-// partial sum (1: a sum per tile, without gaps).
+// The tile sums of a large plan, joined in groups of kJoinGroup tiles before
+// the last join: a wave per group, a slot per (group, descriptor) as in
+// grad_norm_kernel. One workgroup joining the 486,186 tile sums of the GPT-2
+// small gradients by itself took 210 us, this and the last join take 6.
 template <int NT>
-__global__ __launch_bounds__(kFinishThreads) void norm_finish_kernel(
-    const double *__restrict__ partial, int64_t slots, const SegDesc *__restrict__ seg,
-    int32_t group, int64_t tile_elems, int32_t n_params, float *__restrict__ norms,
-    float *__restrict__ param_norms) {
-  __shared__ double parts[kFinishThreads / 64];
-  const int32_t rank = static_cast<int32_t>(blockIdx.y);
-  int64_t i0 = 0, i1 = slots;
-  float *out = norms + rank;
-  if (blockIdx.x > 0) {
-    const int32_t s = static_cast<int32_t>(blockIdx.x) - 1;
+__global__ __launch_bounds__(64) void norm_join_kernel(
+    const double *__restrict__ tile_sums, int64_t tiles, const SegDesc *__restrict__ seg,
+    const int32_t *__restrict__ tile_seg, int64_t map_stride, int64_t tile_elems,
+    double *__restrict__ joined) {
+  const int lane = static_cast<int>(threadIdx.x);
+  const int64_t g = blockIdx.x;
+  const int64_t end = std::min((g + 1) * kJoinGroup, tiles);
+  int32_t s = tile_seg[tile_map_index(g * kJoinGroup, map_stride)];
+  for (int64_t t = g * kJoinGroup; t < end; ++s) {
     const SegDesc d = seg[s];
-    const int64_t a = d.tile_begin, b = a + (d.len + tile_elems - 1) / tile_elems;
-    i0 = group == 1 ? a : a / group + s;
-    i1 = group == 1 ? b : (b - 1) / group + s + 1;
-    out = param_norms + static_cast<int64_t>(rank) * n_params + d.param;
+    const int64_t seg_end = d.tile_begin + (d.len + tile_elems - 1) / tile_elems;
+    const int64_t stop = std::min(seg_end, end);
+    NormSum<NT> sum;
+#pragma unroll
+    for (int k = 0; k < kJoinGroup / 64; ++k) {
+      if (t + k * 64 + lane < stop) sum.join_part(tile_sums[t + k * 64 + lane]);
+    }
+    join_wave(sum);
+    if (lane == 0) {
+      joined[g + s] = sum.part();
+      if (stop == end && stop == seg_end) joined[g + s + 1] = 0.0;
+    }
+    t = stop;
   }
-  const double *src = partial + static_cast<int64_t>(rank) * slots;
+}
+
+// The sum of partial[i0 .. i1) over `width` threads, of which this is `me`;
+// the loads of a batch are in flight together.
+template <int NT>
+__device__ __forceinline__ NormSum<NT> join_range(const double *__restrict__ partial, int64_t i0,
+                                                  int64_t i1, int me, int width) {
+  constexpr int kLoads = 8;
   NormSum<NT> sum;
-  for (int64_t i = i0 + threadIdx.x; i < i1; i += kFinishThreads) sum.join_part(src[i]);
-  join_wave(sum);
-  if ((threadIdx.x & 63) == 0) parts[threadIdx.x >> 6] = sum.part();
+  for (int64_t i = i0 + me; i < i1; i += kLoads * width) {
+    double x[kLoads];
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) {
+      const int64_t j = i + static_cast<int64_t>(k) * width;
+      x[k] = j < i1 ? partial[j] : 0.0;
+    }
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) sum.join_part(x[k]);
+  }
+  return sum;
+}
+
+// Block 0 joins all of a rank's partial sums into its norm; the other blocks
+// take kFinishWaves descriptors each and join those of each parameter, a wave
+// per parameter, or the whole block for one of more than kWaveSlots sums.
+// `group` is the tiles per partial sum (1: a sum per tile, without gaps).
+template <int NT>
+__global__ __launch_bounds__(64 * kFinishWaves) void norm_finish_kernel(
+    const double *__restrict__ partial, int64_t slots, const SegDesc *__restrict__ seg,
+    int32_t nseg, int32_t group, int64_t tile_elems, int32_t n_params,
+    float *__restrict__ norms, float *__restrict__ param_norms) {
+  __shared__ double parts[kFinishWaves];
+  const int32_t rank = static_cast<int32_t>(blockIdx.y);
+  const int tid = static_cast<int>(threadIdx.x);
+  const double *src = partial + static_cast<int64_t>(rank) * slots;
+  auto block_norm = [&](int64_t i0, int64_t i1, float *out) {
+    NormSum<NT> sum = join_range<NT>(src, i0, i1, tid, 64 * kFinishWaves);
+    join_wave(sum);
+    if ((tid & 63) == 0) parts[tid >> 6] = sum.part();
+    __syncthreads();
+    if (tid == 0) {
+      NormSum<NT> all;
+      for (int w = 0; w < kFinishWaves; ++w) all.join_part(parts[w]);
+      *out = all.norm();
+    }
+    __syncthreads();
+  };
+  if (blockIdx.x == 0) {
+    block_norm(0, slots, norms + rank);
+    return;
+  }
+  const int32_t s0 = (static_cast<int32_t>(blockIdx.x) - 1) * kFinishWaves;
+  const auto range_of = [&](int32_t i, int64_t &i0, int64_t &i1) {
+    const SegDesc d = seg[i];
+    const int64_t a = d.tile_begin, b = a + (d.len + tile_elems - 1) / tile_elems;
+    i0 = group == 1 ? a : a / group + i;
+    i1 = group == 1 ? b : (b - 1) / group + i + 1;
+    return param_norms + static_cast<int64_t>(rank) * n_params + d.param;
+  };
+  __shared__ int32_t large[kFinishWaves];
+  const int32_t mine = s0 + (tid >> 6);
+  int64_t i0 = 0, i1 = 0;
+  if (mine < nseg) {
+    float *out = range_of(mine, i0, i1);
+    if (i1 - i0 <= kWaveSlots) {
+      NormSum<NT> sum = join_range<NT>(src, i0, i1, tid & 63, 64);
+      join_wave(sum);
+      if ((tid & 63) == 0) *out = sum.norm();
+    }
+  }
+  if ((tid & 63) == 0) large[tid >> 6] = i1 - i0 > kWaveSlots;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    NormSum<NT> all;
-    for (int w = 0; w < kFinishThreads / 64; ++w) all.join_part(parts[w]);
-    *out = all.norm();
+  for (int k = 0; k < kFinishWaves; ++k) {
+    if (!large[k]) continue;  // the same for every thread
+    float *out = range_of(s0 + k, i0, i1);
+    block_norm(i0, i1, out);
   }
 }
 
@@ -339,11 +416,51 @@ ddp_status launch_finish_nt(const PlanTiles &t, const double *partial, int64_t s
                           d_param_norms, n);
     if (s != DDP_OK) return s;
   }
-  const uint32_t blocks = 1 + (d_param_norms != nullptr ? static_cast<uint32_t>(t.nseg) : 0);
-  return launch(norm_finish_kernel<NT>, dim3(blocks, static_cast<uint32_t>(ranks)),
-                dim3(kFinishThreads), stream, timer, last, "norm_finish_kernel launch", partial,
-                slots, t.seg, group, bucket_tile_elems(kVecBytes / t.elem_bytes), t.n_params,
-                d_norms, d_param_norms);
+  const int64_t tile_elems = bucket_tile_elems(kVecBytes / t.elem_bytes);
+  const int64_t blocks = 1 + (d_param_norms != nullptr ? ceil_div(t.nseg, kFinishWaves) : 0);
+  return launch(norm_finish_kernel<NT>,
+                dim3(static_cast<uint32_t>(blocks), static_cast<uint32_t>(ranks)),
+                dim3(64 * kFinishWaves), stream, timer, last, "norm_finish_kernel launch",
+                partial, slots, t.seg, t.nseg, group, tile_elems, t.n_params, d_norms,
+                d_param_norms);
+}
+
+// The tile sums of a plan in `partial` into its norms: at once, or through
+// norm_join_kernel, whose sums follow the tiles'. Up to kNormJoinTiles sums
+// one more launch costs more than it saves.
+template <int NT>
+ddp_status launch_tile_finish_nt(const PlanTiles &t, double *partial, float *d_norm,
+                                 float *d_param_norms, hipStream_t stream, CallTimer &timer,
+                                 bool last) {
+  if (t.tiles <= kNormJoinTiles) {
+    return launch_finish_nt<NT>(t, partial, t.tiles, 1, 1, d_norm, d_param_norms, stream, timer,
+                                last);
+  }
+  const int64_t groups = ceil_div(t.tiles, kJoinGroup);
+  double *joined = partial + t.tiles;
+  ddp_status s = launch(norm_join_kernel<NT>, dim3(static_cast<uint32_t>(groups)), dim3(64),
+                        stream, timer, false, "norm_join_kernel launch", partial, t.tiles, t.seg,
+                        t.tile_seg, t.map_stride, bucket_tile_elems(kVecBytes / t.elem_bytes),
+                        joined);
+  if (s != DDP_OK) return s;
+  return launch_finish_nt<NT>(t, joined, groups + t.nseg, kJoinGroup, 1, d_norm, d_param_norms,
+                              stream, timer, last);
+}
+
+ddp_status launch_tile_finish(const PlanTiles &t, int32_t norm_type, double *partial,
+                              float *d_norm, float *d_param_norms, hipStream_t stream,
+                              CallTimer &timer, bool last) {
+  switch (norm_type) {
+    case DDP_NORM_L2:
+      return launch_tile_finish_nt<DDP_NORM_L2>(t, partial, d_norm, d_param_norms, stream, timer,
+                                                last);
+    case DDP_NORM_L1:
+      return launch_tile_finish_nt<DDP_NORM_L1>(t, partial, d_norm, d_param_norms, stream, timer,
+                                                last);
+    default:
+      return launch_tile_finish_nt<DDP_NORM_INF>(t, partial, d_norm, d_param_norms, stream, timer,
+                                                 last);
+  }
 }
 
 ddp_status launch_finish(const PlanTiles &t, int32_t norm_type, const double *partial,
@@ -504,8 +621,8 @@ extern "C" ddp_status ddp_grad_norm_finish(const ddp_plan *plan, int32_t norm_ty
     s = check_scratch(what, workspace, workspace_bytes, ddp_sync_norm_workspace(plan));
   }
   if (s != DDP_OK) return s;
-  return launch_finish(t, norm_type, static_cast<double *>(workspace), t.tiles, 1, 1, d_norm,
-                       d_param_norms, stream, timer, true);
+  return launch_tile_finish(t, norm_type, static_cast<double *>(workspace), d_norm,
+                            d_param_norms, stream, timer, true);
 }
 
 extern "C" ddp_status ddp_allreduce_clip(const ddp_plan *plan, int32_t p,
@@ -541,8 +658,8 @@ extern "C" ddp_status ddp_allreduce_clip(const ddp_plan *plan, int32_t p,
                           DDPSIM_BUCKET_MAX_WORKGROUPS, &epi, &timer, false);
     if (s != DDP_OK) return s;
   }
-  s = launch_finish(t, norm_type, epi.partial, t.tiles, 1, 1, d_norm, d_param_norms, stream,
-                    timer, t.tiles == 0);
+  s = launch_tile_finish(t, norm_type, epi.partial, d_norm, d_param_norms, stream, timer,
+                         t.tiles == 0);
   if (s != DDP_OK || nb == 0) return s;
   epi.mode = kSyncScale;
   s = allreduce_buckets(plan, 0, nb, p, d_grad_ptrs, dtype, avg_mode, tokens, stream, stats,

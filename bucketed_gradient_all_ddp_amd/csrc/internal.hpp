@@ -193,6 +193,10 @@ bool plan_tiles(const ddp_plan *plan, PlanTiles *out);
 constexpr int kNormGroup = 16;
 int64_t norm_groups(const PlanTiles &t);
 int64_t norm_slots(const PlanTiles &t);
+// The all-reduce's norm: a sum per tile, then, beyond kNormJoinTiles tiles, a
+// sum per kNormJoinGroup tiles and parameter in slots of the same kind.
+constexpr int kNormJoinGroup = 256;
+constexpr int64_t kNormJoinTiles = 32768;
 
 // What a bucket launch does with the averaged values besides storing them.
 //   kSyncPlain   the all-reduce alone
@@ -200,6 +204,9 @@ int64_t norm_slots(const PlanTiles &t);
 //   kFoldNorm    each tile's part of the norm only; the gradients stay
 //   kSyncScale   the all-reduce of the average times the clip coefficient of
 //                *norm
+#ifndef DDPSIM_FOLD_WGS_PER_CU
+#define DDPSIM_FOLD_WGS_PER_CU 18  // workgroups resident per CU of kFoldNorm
+#endif
 enum SyncMode : int32_t { kSyncPlain = 0, kSyncNorm = 1, kFoldNorm = 2, kSyncScale = 3 };
 struct SyncEpilogue {
   int32_t mode;

@@ -188,7 +188,9 @@ extern "C" size_t ddp_grad_norm_workspace(const ddp_plan *plan, int32_t p) {
 extern "C" size_t ddp_sync_norm_workspace(const ddp_plan *plan) {
   PlanTiles t;
   if (!plan_tiles(plan, &t)) return 0;
-  return sizeof(double) * static_cast<size_t>(t.tiles);
+  int64_t sums = t.tiles;
+  if (t.tiles > kNormJoinTiles) sums += ceil_div(t.tiles, kNormJoinGroup) + t.nseg;
+  return sizeof(double) * static_cast<size_t>(sums);
 }
 
 extern "C" size_t ddp_plan_segment_bytes(const ddp_plan *plan, int32_t p) {

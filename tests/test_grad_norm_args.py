@@ -35,6 +35,10 @@ def test_workspace_sizes():
             assert plan.grad_norm_workspace(p) == 8 * p * (-(-tiles // 16) + live)
         assert plan.grad_norm_workspace(0) == 0 and plan.grad_norm_workspace(65) == 0
         assert plan.sync_norm_workspace() == 8 * tiles
+    # past 32768 tiles: a second level of sums per 256 tiles and parameter
+    assert ddp.ddp_bucket_plan([32768 * 256, 0], 4).sync_norm_workspace() == 8 * 32768
+    big = ddp.ddp_bucket_plan([32768 * 256, 0, 1], 4)
+    assert big.sync_norm_workspace() == 8 * (32769 + 129 + 2)
     L = load_library()
     assert L.ddp_grad_norm_workspace(None, 4) == 0 and L.ddp_sync_norm_workspace(None) == 0
     empty = ddp.ddp_bucket_plan([], 4)
