@@ -11,7 +11,9 @@ raises ImportError rather than falling back to anything else.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 from typing import List, Optional, Sequence, Tuple
 
@@ -169,10 +171,12 @@ def _check(status: int, func: str) -> None:
 
 
 def _stream(stream) -> Optional[int]:
-    import torch
-
     if stream is None:
-        stream = torch.cuda.current_stream()
+        import torch
+
+        # the current stream's handle; torch.cuda.current_stream() builds a
+        # Stream object around it, which costs as much as a kernel launch
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -278,6 +282,7 @@ class Plan:
         self._table = None
         self._segments = None
         self._numels = None
+        self._num_params = None
 
     def __del__(self):
         if getattr(self, "_h", None) and self._h.value and _lib is not None:
@@ -290,7 +295,9 @@ class Plan:
 
     @property
     def num_params(self) -> int:
-        return load_library().ddp_plan_num_params(self._h)
+        if self._num_params is None:
+            self._num_params = load_library().ddp_plan_num_params(self._h)
+        return self._num_params
 
     @property
     def num_buckets(self) -> int:
@@ -616,14 +623,15 @@ def ddp_allreduce_buckets(plan: Plan, first_bucket: int, n_buckets: int, grad_ta
 # Gradient norm and clipping
 # ---------------------------------------------------------------------------
 
+_SAME_DEVICE = contextlib.nullcontext()
+
+
 def _on_device(tensor):
     """The library launches on the current device: make that the tensor's."""
-    import contextlib
-
     import torch
 
-    if tensor is None or tensor.device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
+    if tensor is None or tensor.get_device() == torch._C._cuda_getDevice():
+        return _SAME_DEVICE
     return torch.cuda.device(tensor.device)
 
 
@@ -639,27 +647,32 @@ def _empty(n: int, dtype, device, stream):
         return torch.empty(n, dtype=dtype, device=device)
 
 
+@functools.lru_cache(maxsize=None)
+def _value_types():
+    import torch
+
+    return (frozenset([torch.float32]), frozenset([torch.bfloat16]))
+
+
 def _check_norm_dtype(table, what: str) -> None:
     """The norm and clip kernels read values, not bytes: float32 or bfloat16
     gradients, all of one type."""
-    import torch
-
     dtypes = getattr(table, "_ddp_dtypes", None)
-    if dtypes and dtypes not in ({torch.float32}, {torch.bfloat16}):
+    if dtypes and dtypes not in _value_types():
         raise TypeError(f"{what}: gradients must all be float32 or all bfloat16, got "
                         f"{sorted(map(str, dtypes))}")
 
 
 def _floats(t, n: int, device, what: str, name: str) -> Optional[int]:
     """Address of a contiguous float32 device tensor of n elements."""
-    import torch
-
     if t is None:
         return None
-    if t.dtype != torch.float32 or not t.is_contiguous() or t.numel() != n:
+    import torch
+
+    if t.dtype is not torch.float32 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{what}: {name} must be a contiguous float32 tensor of {n} elements")
     ptr = _device_ptr(t)
-    if device is not None and t.device != device:
+    if device is not None and t.get_device() != device.index:
         raise ValueError(f"{what}: {name} is on {t.device}, the gradient table on {device}")
     return ptr
 
@@ -670,7 +683,7 @@ def _workspace(t, table, what: str) -> Tuple[Optional[int], int]:
     if not t.is_contiguous():
         raise ValueError(f"{what}: the workspace must be contiguous")
     ptr = _device_ptr(t)
-    if table is not None and t.device != table.device:
+    if table is not None and t.get_device() != table.get_device():
         raise ValueError(f"{what}: the workspace is on {t.device}, the gradient table on "
                          f"{table.device}")
     return ptr, t.numel() * t.element_size()

@@ -117,29 +117,14 @@ __device__ __forceinline__ void fold_vector_per_lane(uint64_t mine, int32_t p, i
   }
 }
 
-// What happens to a finished fp32 value on its way to the ranks: kMode as
-// SyncMode, `sum` this lane's part of the tile's norm, `scale` the clip
-// coefficient.
-template <int kMode, int NT>
-struct TileEpilogue {
-  static constexpr bool kStore = kMode != kFoldNorm;
-  NormSum<NT> sum;
-  float scale = 1.0f;
-  __device__ __forceinline__ float operator()(float y) {
-    if constexpr (kMode == kSyncNorm || kMode == kFoldNorm) sum.add(y);
-    if constexpr (kMode == kSyncScale) y = y * scale;
-    return y;
-  }
-};
-
 // One tile of the plan's numbering; the tile map names the parameter
 // descriptor (index into seg) each tile belongs to.
-template <typename Tr, int VPT, int RB, bool kNT, typename Epilogue>
+template <typename Tr, int VPT, int RB, bool kNT>
 __device__ __forceinline__ void bucket_tile(const SegDesc *__restrict__ seg,
                                             const int32_t *__restrict__ tile_seg,
                                             int64_t map_stride, int32_t tile, int32_t n_params,
                                             const void *const *__restrict__ grads, int32_t p,
-                                            const Divide &div, Epilogue &epi) {
+                                            const Divide &div) {
   constexpr int V = Tr::kVec;
   constexpr int64_t kElemBytes = sizeof(typename Tr::elem);
   const SegDesc d = seg[tile_seg[tile_map_index(tile, map_stride)]];
@@ -166,9 +151,8 @@ __device__ __forceinline__ void bucket_tile(const SegDesc *__restrict__ seg,
     const int64_t j0 = static_cast<int64_t>(t) * kTile;
     const int64_t j1 = std::min(j0 + kTile, d.len);
     for (int64_t j = j0 + tid; j < j1; j += kThr) {
-      const float y =
-          epi(apply_divide(fold_scalar<Tr>(at, p, chunk_of(d.offset, j, d.chunk), j), div));
-      for (int32_t r = 0; Epilogue::kStore && r < p; ++r) Tr::store1(at(r), j, y);
+      const float y = apply_divide(fold_scalar<Tr>(at, p, chunk_of(d.offset, j, d.chunk), j), div);
+      for (int32_t r = 0; r < p; ++r) Tr::store1(at(r), j, y);
     }
     return;
   }
@@ -186,8 +170,8 @@ __device__ __forceinline__ void bucket_tile(const SegDesc *__restrict__ seg,
     const int64_t J = head ? k.s + lane : k.tail_begin + (lane - (V - 1));
     if (J < (head ? k.head_end : k.e)) {
       const float y =
-          epi(apply_divide(fold_scalar<Tr>(at, p, chunk_of(d.offset, J - m, d.chunk), J), div));
-      for (int32_t r = 0; Epilogue::kStore && r < p; ++r) Tr::store1(at(r), J, y);
+          apply_divide(fold_scalar<Tr>(at, p, chunk_of(d.offset, J - m, d.chunk), J), div);
+      for (int32_t r = 0; r < p; ++r) Tr::store1(at(r), J, y);
     }
   }
 
@@ -236,14 +220,9 @@ __device__ __forceinline__ void bucket_tile(const SegDesc *__restrict__ seg,
 #pragma unroll
   for (int u = 0; u < VPT; ++u) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float v = apply_divide(acc[u][e], div);
-      // a lane past the body holds no element
-      acc[u][e] = ok[u] ? epi(v) : v;
-    }
+    for (int e = 0; e < V; ++e) acc[u][e] = apply_divide(acc[u][e], div);
     y[u] = Tr::narrow(acc[u]);
   }
-  if constexpr (!Epilogue::kStore) return;
   const int32_t rot = store_rotation(p, tile);
   for (int32_t r = 0; r < p; ++r) {
     void *dst = lat(ring_rank(rot, r, p));
@@ -265,32 +244,214 @@ __global__ __launch_bounds__(kBucketThreads) void bucket_allreduce_kernel(
     const void *const *__restrict__ grads, int32_t p, Divide div) {
   for (int32_t w = static_cast<int32_t>(blockIdx.x); w < n_tiles;
        w += static_cast<int32_t>(gridDim.x)) {
-    TileEpilogue<kSyncPlain, DDP_NORM_L2> epi;
     bucket_tile<Tr, VPT, RB, kNT>(seg, tile_seg, map_stride, tile_base + w, n_params, grads, p,
-                                  div, epi);
+                                  div);
   }
 }
 
-// The same tiles with an epilogue: each workgroup (one wave) leaves its
-// tile's part of the norm in partial[tile], or scales by the coefficient.
-template <typename Tr, int VPT, int RB, bool kNT, int kMode, int NT>
-__global__ __launch_bounds__(kBucketThreads) void bucket_epilogue_kernel(
+// What becomes of a finished fp32 value on its way to the ranks: kMode as
+// SyncMode, `sum` this lane's part of the norm, `scale` the clip coefficient.
+template <int kMode, int NT>
+struct Epilogue {
+  static constexpr bool kNorm = kMode != kSyncScale;
+  static constexpr bool kSpread = kMode == kSyncNorm || kMode == kSyncScale;  // to every rank
+  static constexpr bool kStage = kMode == kStageNorm;
+  NormSum<NT> sum;
+  float scale = 1.0f;
+  __device__ __forceinline__ float operator()(float y) {
+    if constexpr (kNorm) sum.add(y);
+    if constexpr (kMode == kSyncScale) y = y * scale;
+    return y;
+  }
+  template <typename Tr, typename Ptrs>
+  __device__ __forceinline__ void store1(const Ptrs &at, int32_t p, int32_t tile, int64_t i,
+                                         float y) const {
+    if constexpr (kStage) {
+      const int32_t a = stage_rank(p, tile);
+      Tr::stage1(at(a), at(ring_rank(a, 1, p)), i, y);
+    }
+    for (int32_t r = 0; kSpread && r < p; ++r) Tr::store1(at(r), i, y);
+  }
+};
+
+// bucket_tile for up to G consecutive tiles of one parameter, [t, t1) of its
+// own, the first of them tile `tile` of the plan, with an epilogue. One fetch
+// of the addresses serves them all, and G * RB loads are in flight.
+template <typename Tr, int G, int RB, typename Epi>
+__device__ __forceinline__ void bucket_run(const SegDesc &d, int64_t t, int64_t t1, int32_t tile,
+                                           int32_t n_params,
+                                           const void *const *__restrict__ grads, int32_t p,
+                                           const Divide &div, Epi &epi) {
+  constexpr int V = Tr::kVec;
+  constexpr int64_t kElemBytes = sizeof(typename Tr::elem);
+  constexpr int64_t kTile = 64 * V;
+  const int lane = static_cast<int>(threadIdx.x) & 63;
+  const uint64_t mine =
+      lane < p ? reinterpret_cast<uint64_t>(grads[static_cast<int64_t>(lane) * n_params + d.param])
+               : 0;
+  const uint64_t phase = __builtin_amdgcn_readlane(static_cast<uint32_t>(mine), 0) %
+                         static_cast<uint32_t>(kVecBytes);
+  if (!__all(lane >= p || mine % kVecBytes == phase)) {
+    const GradPtrs at{grads, n_params, d.param, 0};
+    const int64_t j1 = std::min(t1 * kTile, d.len);
+    for (int64_t j = t * kTile + lane; j < j1; j += 64) {
+      const float y =
+          epi(apply_divide(fold_scalar<Tr>(at, p, chunk_of(d.offset, j, d.chunk), j), div));
+      epi.template store1<Tr>(at, p, tile + static_cast<int32_t>(j / kTile - t), j, y);
+    }
+    return;
+  }
+  // indices from the aligned address m elements below each rank's base
+  const int64_t m = static_cast<int64_t>(phase) / kElemBytes;
+  const ChunkSpan k = make_span(m, d.len + m, V);
+  if (t == 0 && lane >= 64 - 2 * (V - 1)) {
+    const GradPtrs at{grads, n_params, d.param, m * kElemBytes};
+    const int i = lane - (64 - 2 * (V - 1));
+    const bool head = i < V - 1;
+    const int64_t J = head ? k.s + i : k.tail_begin + (i - (V - 1));
+    if (J < (head ? k.head_end : k.e)) {
+      const float y =
+          epi(apply_divide(fold_scalar<Tr>(at, p, chunk_of(d.offset, J - m, d.chunk), J), div));
+      epi.template store1<Tr>(at, p, tile, J, y);
+    }
+  }
+  const int64_t v0 = k.vs / V + t * 64;
+  const int64_t v1 = std::min(k.ve / V, k.vs / V + t1 * 64);
+  if (v0 >= v1) return;
+  int64_t vi[G];
+  bool ok[G];
+#pragma unroll
+  for (int u = 0; u < G; ++u) {
+    vi[u] = v0 + u * 64 + lane;
+    ok[u] = vi[u] < v1;
+  }
+  const uint64_t shifted = mine - static_cast<uint64_t>(m * kElemBytes);
+  const LanePtrs lat{shifted};
+  const int32_t c_first = chunk_of(d.offset, v0 * V - m, d.chunk);
+  const int32_t c_last = chunk_of(d.offset, v1 * V - 1 - m, d.chunk);
+  float acc[G][V];
+  if (c_first == c_last) {
+    fold_vectors<Tr, G, RB, true>(lat, p, c_first, vi, ok, acc);
+  } else {
+#pragma unroll
+    for (int u = 0; u < G; ++u) {
+      // a lane past the body computes with the last vector (never stored)
+      const int64_t j0 = (ok[u] ? vi[u] : v1 - 1) * V - m;
+      const int32_t c0 = chunk_of(d.offset, j0, d.chunk);
+      int32_t dist[V];
+      int64_t next = (static_cast<int64_t>(c0) + 1) * d.chunk - d.offset;
+      int32_t dd = 0;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        while (j0 + e >= next) {
+          ++dd;
+          next += d.chunk;
+        }
+        dist[e] = dd;
+      }
+      fold_vector_per_lane<Tr, (RB > 8 ? RB : 8), true>(shifted, p, c0, dist, vi[u], ok[u], acc[u]);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < G; ++u) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float v = apply_divide(acc[u][e], div);
+      acc[u][e] = ok[u] ? epi(v) : v;
+    }
+  }
+  if constexpr (Epi::kStage) {
+#pragma unroll
+    for (int u = 0; u < G; ++u) {
+      const int32_t a = stage_rank(p, tile + u);
+      uint4 hi, lo;
+      Tr::split(acc[u], hi, lo);
+      // past the caches: 0.73 ms for GPT-2 small on 8 ranks, 0.83 with
+      // ordinary stores
+      if (ok[u]) {
+        store_vec<true>(lat(a), vi[u], hi);
+        if constexpr (Tr::kStageRanks == 2) store_vec<true>(lat(ring_rank(a, 1, p)), vi[u], lo);
+      }
+    }
+  }
+  if constexpr (Epi::kSpread) {
+    uint4 y[G];
+#pragma unroll
+    for (int u = 0; u < G; ++u) y[u] = Tr::narrow(acc[u]);
+    const int32_t rot = store_rotation(p, tile);
+    for (int32_t r = 0; r < p; ++r) {
+      void *dst = lat(ring_rank(rot, r, p));
+#pragma unroll
+      for (int u = 0; u < G; ++u) {
+        if (ok[u]) store_vec<true>(dst, vi[u], y[u]);
+      }
+    }
+  }
+}
+
+// The all-reduce's tiles with an epilogue, G consecutive ones per wave: each
+// wave leaves its tiles' part of the norm in partial (the sum of a run of one
+// parameter's tiles at its first tile, zeros at the others), or scales by the
+// coefficient.
+template <typename Tr, int G, int RB, int kMode, int NT>
+__global__ __launch_bounds__(64) void bucket_epilogue_kernel(
     const SegDesc *__restrict__ seg, const int32_t *__restrict__ tile_seg, int64_t map_stride,
     int32_t tile_base, int32_t n_tiles, int32_t n_params,
     const void *const *__restrict__ grads, int32_t p, Divide div, double *__restrict__ partial,
-    const float *__restrict__ norm, float max_norm, float eps) {
-  static_assert(kBucketThreads == 64, "a tile's sum is joined within one wave");
-  for (int32_t w = static_cast<int32_t>(blockIdx.x); w < n_tiles;
+    const float *__restrict__ norm, float max_norm, float eps, bool runs) {
+  static_assert(kBucketThreads == 64 && kBucketVpt == 1, "a tile is one vector per lane");
+  const int32_t groups = (n_tiles + G - 1) / G;
+  for (int32_t w = static_cast<int32_t>(blockIdx.x); w < groups;
        w += static_cast<int32_t>(gridDim.x)) {
-    TileEpilogue<kMode, NT> epi;
-    if constexpr (kMode == kSyncScale) epi.scale = clip_coefficient(*norm, max_norm, eps);
-    bucket_tile<Tr, VPT, RB, kNT>(seg, tile_seg, map_stride, tile_base + w, n_params, grads, p,
-                                  div, epi);
-    if constexpr (kMode != kSyncScale) {
-      join_wave(epi.sum);
-      if (threadIdx.x == 0) partial[tile_base + w] = epi.sum.part();
-    }
+    const int32_t g = runs ? static_cast<int32_t>(xcd_run<kXcdRun>(w, groups)) : w;
+    int32_t tile = tile_base + g * G;
+    const int32_t end = std::min(tile + G, tile_base + n_tiles);
+    int32_t s = tile_seg[tile_map_index(tile, map_stride)];
+    do {
+      const SegDesc d = seg[s++];
+      constexpr int64_t kTile = 64 * Tr::kVec;
+      const int64_t t = tile - d.tile_begin;
+      const int64_t t1 = std::min((d.len + kTile - 1) / kTile, t + (end - tile));
+      Epilogue<kMode, NT> epi;
+      if constexpr (kMode == kSyncScale) epi.scale = clip_coefficient(*norm, max_norm, eps);
+      bucket_run<Tr, G, RB>(d, t, t1, tile, n_params, grads, p, div, epi);
+      const int32_t count = static_cast<int32_t>(t1 - t);
+      if constexpr (kMode != kSyncScale) {
+        join_wave(epi.sum);
+        if (static_cast<int32_t>(threadIdx.x) < count) {
+          partial[tile + threadIdx.x] = threadIdx.x == 0 ? epi.sum.part() : 0.0;
+        }
+      }
+      tile += count;
+    } while (tile < end);
   }
+}
+
+// Tiles per wave of an epilogue launch and rank loads in flight of each.
+// With few ranks a tile is little work next to fetching its descriptor and
+// addresses, so that a wave takes as many as keep about 8 loads in flight,
+// if they leave waves enough and its parameters are not smaller. First pass
+// on GPT-2 small fp32, 1 / 2 / 4 tiles per wave: 0.34 / 0.19 / 0.12 ms for
+// one rank, 0.41 / 0.28 / 0.23 for 2, 0.45 / 0.33 / 0.35 for 3, 0.47 / 0.41 /
+// 0.42 for 4, 0.49 / 0.51 / 0.53 for 5.
+// With many ranks and few tiles, one wave's folds follow one another with
+// the chip nearly empty: 32 loads in flight instead of 8.
+#ifndef DDPSIM_FULL_TILES
+#define DDPSIM_FULL_TILES 16384
+#endif
+#ifndef DDPSIM_FEW_TILES
+#define DDPSIM_FEW_TILES 4096
+#endif
+constexpr int64_t kFullTiles = DDPSIM_FULL_TILES;
+constexpr int64_t kFewTiles = DDPSIM_FEW_TILES;
+struct WaveShape {
+  int32_t tiles, loads;
+};
+WaveShape wave_shape(int32_t p, int64_t tiles, int64_t params) {
+  int32_t g = p <= 2 ? 4 : p <= 4 ? 2 : 1;
+  while (g > 1 && (tiles < g * kFullTiles || tiles < g * params)) g /= 2;
+  if (p > 8 && tiles < kFewTiles) return {1, 32};
+  return {g, 8 / g};
 }
 
 // The arguments of one bucket launch, and its kernel by type, mode and norm.
@@ -305,42 +466,54 @@ struct BucketLaunch {
   dim3 grid;
   size_t lds;
   hipStream_t stream;
+  WaveShape shape;
 };
 
-template <typename Tr, int kMode, int NT>
+template <typename Tr, int G, int RB, int kMode, int NT>
 ddp_status launch_epilogue(const BucketLaunch &b, const SyncEpilogue &e, CallTimer &timer,
                            bool last) {
-  return launch_lds(bucket_epilogue_kernel<Tr, kBucketVpt, kBucketRb, kBucketNt, kMode, NT>,
-                    b.grid, dim3(kBucketThreads), b.lds, b.stream, timer, last,
-                    "bucket_epilogue_kernel launch", b.seg, b.tile_seg, b.map_stride, b.tile0,
-                    b.tiles, b.n_params, b.grads, b.p, b.div, e.partial, e.norm, e.max_norm,
-                    e.eps);
+  return launch_lds(bucket_epilogue_kernel<Tr, G, RB, kMode, NT>, b.grid, dim3(64), b.lds,
+                    b.stream, timer, last, "bucket_epilogue_kernel launch", b.seg, b.tile_seg,
+                    b.map_stride, b.tile0, b.tiles, b.n_params, b.grads, b.p, b.div, e.partial,
+                    e.norm, e.max_norm, e.eps, e.runs);
 }
 
-template <typename Tr, int kMode>
+template <typename Tr, int G, int RB, int kMode>
 ddp_status launch_norm_type(const BucketLaunch &b, const SyncEpilogue &e, CallTimer &timer,
                             bool last) {
   switch (e.norm_type) {
-    case DDP_NORM_L2: return launch_epilogue<Tr, kMode, DDP_NORM_L2>(b, e, timer, last);
-    case DDP_NORM_L1: return launch_epilogue<Tr, kMode, DDP_NORM_L1>(b, e, timer, last);
-    default: return launch_epilogue<Tr, kMode, DDP_NORM_INF>(b, e, timer, last);
+    case DDP_NORM_L2: return launch_epilogue<Tr, G, RB, kMode, DDP_NORM_L2>(b, e, timer, last);
+    case DDP_NORM_L1: return launch_epilogue<Tr, G, RB, kMode, DDP_NORM_L1>(b, e, timer, last);
+    default: return launch_epilogue<Tr, G, RB, kMode, DDP_NORM_INF>(b, e, timer, last);
   }
+}
+
+// kFoldNorm and kSyncScale are the two passes of a single rank.
+template <typename Tr, int G, int RB>
+ddp_status launch_mode(const BucketLaunch &b, const SyncEpilogue &e, CallTimer &timer,
+                       bool last) {
+  if (e.mode == kSyncNorm) return launch_norm_type<Tr, G, RB, kSyncNorm>(b, e, timer, last);
+  if (e.mode == kStageNorm) return launch_norm_type<Tr, G, RB, kStageNorm>(b, e, timer, last);
+  if constexpr (G != 2 && RB != 32) {
+    if (e.mode == kFoldNorm) return launch_norm_type<Tr, G, RB, kFoldNorm>(b, e, timer, last);
+    return launch_epilogue<Tr, G, RB, kSyncScale, DDP_NORM_L2>(b, e, timer, last);
+  }
+  return fail(DDP_EINVAL, "two folds of %d ranks", b.p);
 }
 
 template <typename Tr>
 ddp_status launch_bucket(const BucketLaunch &b, const SyncEpilogue *e, CallTimer &timer,
                          bool last) {
-  if (e == nullptr || e->mode == kSyncPlain) {
+  if (e == nullptr) {
     return launch_lds(bucket_allreduce_kernel<Tr, kBucketVpt, kBucketRb, kBucketNt>, b.grid,
                       dim3(kBucketThreads), b.lds, b.stream, timer, last,
                       "bucket_allreduce_kernel launch", b.seg, b.tile_seg, b.map_stride, b.tile0,
                       b.tiles, b.n_params, b.grads, b.p, b.div);
   }
-  switch (e->mode) {
-    case kSyncNorm: return launch_norm_type<Tr, kSyncNorm>(b, *e, timer, last);
-    case kFoldNorm: return launch_norm_type<Tr, kFoldNorm>(b, *e, timer, last);
-    default: return launch_epilogue<Tr, kSyncScale, DDP_NORM_L2>(b, *e, timer, last);
-  }
+  if (b.shape.loads == 32) return launch_mode<Tr, 1, 32>(b, *e, timer, last);
+  if (b.shape.tiles == 4) return launch_mode<Tr, 4, 2>(b, *e, timer, last);
+  if (b.shape.tiles == 2) return launch_mode<Tr, 2, 4>(b, *e, timer, last);
+  return launch_mode<Tr, 1, 8>(b, *e, timer, last);
 }
 
 }  // namespace
@@ -410,26 +583,27 @@ ddp_status allreduce_buckets(const ddp_plan *plan, int32_t first_bucket, int32_t
   }
   if (tiles == 0) return DDP_OK;
   (void)seg0;
-  (void)nseg;
   const SegDesc *seg = static_cast<const SegDesc *>(table);
   int64_t map_stride = 0;
   const int32_t *tile_seg = plan_tile_map(plan, &map_stride);
   const void *const *grads = d_grad_ptrs;
-  const int32_t blocks = max_workgroups > 0 ? std::min(tiles, max_workgroups) : tiles;
+  const WaveShape shape = epi == nullptr ? WaveShape{1, kBucketRb} : wave_shape(p, tiles, nseg);
+  const int32_t units = (tiles - 1) / shape.tiles + 1;
+  const int32_t blocks = max_workgroups > 0 ? std::min(units, max_workgroups) : units;
   const dim3 grid(static_cast<uint32_t>(blocks));
   // Each workgroup keeps 2p streams of 1 KiB in flight (p loads, p
   // stores); a CU full of them (32 one-wave workgroups) puts more streams on
   // every HBM channel than it keeps rows open. Bounding residency at 11 per
   // CU raised the GPT-2 p=8 launch from 5.76 to 6.05 TB/s and the Llama bf16
-  // buckets by 3-4%; 6 per CU starved the channels (5.2).
-  // A fold that stores nothing has p streams per workgroup: bounded at 11 it
-  // read the 8 ranks' GPT-2 gradients at 5.3 TB/s, at 14, 18 and 24 per CU at
-  // 6.5, 6.9 and 6.8 (Llama layers in bf16 4.7, and 5.9, 6.3, 6.3).
-  const bool reads = epi != nullptr && epi->mode == kFoldNorm;
+  // buckets by 3-4%; 6 per CU starved the channels (5.2). A pass that stores
+  // to one or two ranks or none has half as many: bounded at 11 it read the 8
+  // ranks' GPT-2 gradients at 5.3 TB/s, at 14, 18 and 24 per CU at 6.5, 6.9
+  // and 6.8 (Llama layers in bf16 4.7, and 5.9, 6.3, 6.3).
+  const bool reads = epi != nullptr && (epi->mode == kFoldNorm || epi->mode == kStageNorm);
   const size_t lds = residency_lds(
-      fold_residency(reads ? DDPSIM_FOLD_WGS_PER_CU : DDPSIM_BUCKET_WGS_PER_CU, p));
-  const BucketLaunch launch = {seg,   tile_seg, map_stride, tile0, tiles, n_params,
-                               grads, p,        div,        grid,  lds,   stream};
+      fold_residency(reads ? DDPSIM_FOLD_WGS_PER_CU : DDPSIM_BUCKET_WGS_PER_CU, p * shape.tiles));
+  const BucketLaunch launch = {seg,   tile_seg, map_stride, tile0, tiles,  n_params, grads,
+                               p,     div,      grid,       lds,   stream, shape};
   return dtype == DDP_F32 ? launch_bucket<F32Traits>(launch, epi, timer, last)
                           : launch_bucket<BF16Traits>(launch, epi, timer, last);
 }

@@ -117,8 +117,10 @@ bool plan_tiles(const ddp_plan *plan, PlanTiles *out) {
   out->elem_bytes = plan->elem_bytes;
   out->seg_p = plan->seg_p;
   const int64_t tile_elems = bucket_tile_elems(kVecBytes / plan->elem_bytes);
+  out->whole_lines = true;
   for (int64_t n : plan->numel) {
     if (n == 0) continue;
+    if (n * plan->elem_bytes % kLineBytes != 0) out->whole_lines = false;
     ++out->nseg;
     out->tiles += ceil_div(n, tile_elems);
     out->elems += n;
