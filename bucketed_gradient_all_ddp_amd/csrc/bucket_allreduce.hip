@@ -29,9 +29,7 @@
 // in device memory (SyncMode).
 #include <algorithm>
 
-#include "fold.hpp"
-#include "internal.hpp"
-#include "norm.hpp"
+#include "bucket_run.hpp"
 
 namespace ddpsim {
 int32_t plan_num_buckets(const ddp_plan *plan);
@@ -42,80 +40,6 @@ bool plan_segment_info(const ddp_plan *plan, int32_t b, int32_t *first, int32_t 
                        int32_t *elem_bytes);
 
 namespace {
-
-// Element j of a parameter at bucket offset `off` is in ring chunk
-// (off + j) / C; j may run past the parameter by a few elements (a clamped
-// lane), which only moves the chunk of results that are never stored.
-__device__ __forceinline__ int32_t chunk_of(int64_t off, int64_t j, int64_t C) {
-  return static_cast<int32_t>((off + j) / C);
-}
-
-// The fold of one lane's vectors when the ranks' order differs between
-// lanes: lane-held rank addresses (lane r holds rank r's, moved back by the
-// alignment shift) are fetched per lane with a cross-lane read. For vector
-// u, c0 is the chunk of its first element and dist[e] how many chunks later
-// element e's chunk starts (0..V-1; it is below p because every chunk index
-// is). Loads run in the order c0, c0+1, ...; element e adds load t only from
-// t = dist[e] on, then loads 0..dist[e]-1 after the last one, so it sums
-// ranks c0+dist[e], ..., c0+dist[e]+p-1 (mod p) left to right: its own
-// ring order.
-template <typename Tr, int RB, bool kNT>
-__device__ __forceinline__ void fold_vector_per_lane(uint64_t mine, int32_t p, int32_t c0,
-                                                     const int32_t (&dist)[Tr::kVec],
-                                                     int64_t vi, bool ok,
-                                                     float (&acc)[Tr::kVec]) {
-  constexpr int V = Tr::kVec;
-  static_assert(RB >= V - 1, "the first batch must hold the loads added last");
-#pragma unroll
-  for (int e = 0; e < V; ++e) acc[e] = -0.0f;
-  uint4 keep[V > 1 ? V - 1 : 1];
-  const uint32_t lo = static_cast<uint32_t>(mine);
-  const uint32_t hi = static_cast<uint32_t>(mine >> 32);
-  for (int32_t s0 = 0; s0 < p; s0 += RB) {
-    uint4 x[RB];
-#pragma unroll
-    for (int j = 0; j < RB; ++j) {
-      const bool live = s0 + j < p;  // wave-uniform
-      x[j] = make_uint4(0, 0, 0, 0);
-      if (live) {
-        const int32_t r = ring_rank(c0, s0 + j, p);
-        // every lane takes part in the cross-lane reads (no divergence here)
-        const uint32_t alo = static_cast<uint32_t>(__shfl(static_cast<int>(lo), r, 64));
-        const uint32_t ahi = static_cast<uint32_t>(__shfl(static_cast<int>(hi), r, 64));
-        const void *src =
-            reinterpret_cast<const void *>((static_cast<uint64_t>(ahi) << 32) | alo);
-        if (ok) x[j] = load_vec<kNT>(src, vi);
-      }
-    }
-    if (s0 == 0) {
-#pragma unroll
-      for (int j = 0; j < V - 1; ++j) keep[j] = x[j];
-    }
-#pragma unroll
-    for (int j = 0; j < RB; ++j) {
-      const int32_t t = s0 + j;
-      if (t < p) {
-        float w[V];
-        Tr::widen(x[j], w);
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          if (t >= dist[e]) acc[e] = acc[e] + w[e];
-        }
-      }
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < V - 1; ++j) {
-    if (j < p) {
-      float w[V];
-      Tr::widen(keep[j], w);
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        if (j < dist[e]) acc[e] = acc[e] + w[e];
-      }
-    }
-  }
-}
 
 // One tile of the plan's numbering; the tile map names the parameter
 // descriptor (index into seg) each tile belongs to.
@@ -249,146 +173,6 @@ __global__ __launch_bounds__(kBucketThreads) void bucket_allreduce_kernel(
   }
 }
 
-// What becomes of a finished fp32 value on its way to the ranks: kMode as
-// SyncMode, `sum` this lane's part of the norm, `scale` the clip coefficient.
-template <int kMode, int NT>
-struct Epilogue {
-  static constexpr bool kNorm = kMode != kSyncScale;
-  static constexpr bool kSpread = kMode == kSyncNorm || kMode == kSyncScale;  // to every rank
-  static constexpr bool kStage = kMode == kStageNorm;
-  NormSum<NT> sum;
-  float scale = 1.0f;
-  __device__ __forceinline__ float operator()(float y) {
-    if constexpr (kNorm) sum.add(y);
-    if constexpr (kMode == kSyncScale) y = y * scale;
-    return y;
-  }
-  template <typename Tr, typename Ptrs>
-  __device__ __forceinline__ void store1(const Ptrs &at, int32_t p, int32_t tile, int64_t i,
-                                         float y) const {
-    if constexpr (kStage) {
-      const int32_t a = stage_rank(p, tile);
-      Tr::stage1(at(a), at(ring_rank(a, 1, p)), i, y);
-    }
-    for (int32_t r = 0; kSpread && r < p; ++r) Tr::store1(at(r), i, y);
-  }
-};
-
-// bucket_tile for up to G consecutive tiles of one parameter, [t, t1) of its
-// own, the first of them tile `tile` of the plan, with an epilogue. One fetch
-// of the addresses serves them all, and G * RB loads are in flight.
-template <typename Tr, int G, int RB, typename Epi>
-__device__ __forceinline__ void bucket_run(const SegDesc &d, int64_t t, int64_t t1, int32_t tile,
-                                           int32_t n_params,
-                                           const void *const *__restrict__ grads, int32_t p,
-                                           const Divide &div, Epi &epi) {
-  constexpr int V = Tr::kVec;
-  constexpr int64_t kElemBytes = sizeof(typename Tr::elem);
-  constexpr int64_t kTile = 64 * V;
-  const int lane = static_cast<int>(threadIdx.x) & 63;
-  const uint64_t mine =
-      lane < p ? reinterpret_cast<uint64_t>(grads[static_cast<int64_t>(lane) * n_params + d.param])
-               : 0;
-  const uint64_t phase = __builtin_amdgcn_readlane(static_cast<uint32_t>(mine), 0) %
-                         static_cast<uint32_t>(kVecBytes);
-  if (!__all(lane >= p || mine % kVecBytes == phase)) {
-    const GradPtrs at{grads, n_params, d.param, 0};
-    const int64_t j1 = std::min(t1 * kTile, d.len);
-    for (int64_t j = t * kTile + lane; j < j1; j += 64) {
-      const float y =
-          epi(apply_divide(fold_scalar<Tr>(at, p, chunk_of(d.offset, j, d.chunk), j), div));
-      epi.template store1<Tr>(at, p, tile + static_cast<int32_t>(j / kTile - t), j, y);
-    }
-    return;
-  }
-  // indices from the aligned address m elements below each rank's base
-  const int64_t m = static_cast<int64_t>(phase) / kElemBytes;
-  const ChunkSpan k = make_span(m, d.len + m, V);
-  if (t == 0 && lane >= 64 - 2 * (V - 1)) {
-    const GradPtrs at{grads, n_params, d.param, m * kElemBytes};
-    const int i = lane - (64 - 2 * (V - 1));
-    const bool head = i < V - 1;
-    const int64_t J = head ? k.s + i : k.tail_begin + (i - (V - 1));
-    if (J < (head ? k.head_end : k.e)) {
-      const float y =
-          epi(apply_divide(fold_scalar<Tr>(at, p, chunk_of(d.offset, J - m, d.chunk), J), div));
-      epi.template store1<Tr>(at, p, tile, J, y);
-    }
-  }
-  const int64_t v0 = k.vs / V + t * 64;
-  const int64_t v1 = std::min(k.ve / V, k.vs / V + t1 * 64);
-  if (v0 >= v1) return;
-  int64_t vi[G];
-  bool ok[G];
-#pragma unroll
-  for (int u = 0; u < G; ++u) {
-    vi[u] = v0 + u * 64 + lane;
-    ok[u] = vi[u] < v1;
-  }
-  const uint64_t shifted = mine - static_cast<uint64_t>(m * kElemBytes);
-  const LanePtrs lat{shifted};
-  const int32_t c_first = chunk_of(d.offset, v0 * V - m, d.chunk);
-  const int32_t c_last = chunk_of(d.offset, v1 * V - 1 - m, d.chunk);
-  float acc[G][V];
-  if (c_first == c_last) {
-    fold_vectors<Tr, G, RB, true>(lat, p, c_first, vi, ok, acc);
-  } else {
-#pragma unroll
-    for (int u = 0; u < G; ++u) {
-      // a lane past the body computes with the last vector (never stored)
-      const int64_t j0 = (ok[u] ? vi[u] : v1 - 1) * V - m;
-      const int32_t c0 = chunk_of(d.offset, j0, d.chunk);
-      int32_t dist[V];
-      int64_t next = (static_cast<int64_t>(c0) + 1) * d.chunk - d.offset;
-      int32_t dd = 0;
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        while (j0 + e >= next) {
-          ++dd;
-          next += d.chunk;
-        }
-        dist[e] = dd;
-      }
-      fold_vector_per_lane<Tr, (RB > 8 ? RB : 8), true>(shifted, p, c0, dist, vi[u], ok[u], acc[u]);
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < G; ++u) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float v = apply_divide(acc[u][e], div);
-      acc[u][e] = ok[u] ? epi(v) : v;
-    }
-  }
-  if constexpr (Epi::kStage) {
-#pragma unroll
-    for (int u = 0; u < G; ++u) {
-      const int32_t a = stage_rank(p, tile + u);
-      uint4 hi, lo;
-      Tr::split(acc[u], hi, lo);
-      // past the caches: 0.73 ms for GPT-2 small on 8 ranks, 0.83 with
-      // ordinary stores
-      if (ok[u]) {
-        store_vec<true>(lat(a), vi[u], hi);
-        if constexpr (Tr::kStageRanks == 2) store_vec<true>(lat(ring_rank(a, 1, p)), vi[u], lo);
-      }
-    }
-  }
-  if constexpr (Epi::kSpread) {
-    uint4 y[G];
-#pragma unroll
-    for (int u = 0; u < G; ++u) y[u] = Tr::narrow(acc[u]);
-    const int32_t rot = store_rotation(p, tile);
-    for (int32_t r = 0; r < p; ++r) {
-      void *dst = lat(ring_rank(rot, r, p));
-#pragma unroll
-      for (int u = 0; u < G; ++u) {
-        if (ok[u]) store_vec<true>(dst, vi[u], y[u]);
-      }
-    }
-  }
-}
-
 // The all-reduce's tiles with an epilogue, G consecutive ones per wave: each
 // wave leaves its tiles' part of the norm in partial (the sum of a run of one
 // parameter's tiles at its first tile, zeros at the others), or scales by the
@@ -492,13 +276,17 @@ ddp_status launch_norm_type(const BucketLaunch &b, const SyncEpilogue &e, CallTi
 template <typename Tr, int G, int RB>
 ddp_status launch_mode(const BucketLaunch &b, const SyncEpilogue &e, CallTimer &timer,
                        bool last) {
-  if (e.mode == kSyncNorm) return launch_norm_type<Tr, G, RB, kSyncNorm>(b, e, timer, last);
+  // one rank's gradients are their own average: nothing to write
+  const bool stays = b.p == 1 && b.div.mode == kNone;
+  if (e.mode == kSyncNorm && !stays) {
+    return launch_norm_type<Tr, G, RB, kSyncNorm>(b, e, timer, last);
+  }
   if (e.mode == kStageNorm) return launch_norm_type<Tr, G, RB, kStageNorm>(b, e, timer, last);
-  if constexpr (G != 2 && RB != 32) {
-    if (e.mode == kFoldNorm) return launch_norm_type<Tr, G, RB, kFoldNorm>(b, e, timer, last);
+  if constexpr (RB != 32) {  // many loads in flight are for many ranks
+    if (e.mode != kSyncScale) return launch_norm_type<Tr, G, RB, kFoldNorm>(b, e, timer, last);
     return launch_epilogue<Tr, G, RB, kSyncScale, DDP_NORM_L2>(b, e, timer, last);
   }
-  return fail(DDP_EINVAL, "two folds of %d ranks", b.p);
+  return fail(DDP_EINVAL, "no such launch for %d ranks", b.p);
 }
 
 template <typename Tr>

@@ -10,8 +10,7 @@
 #include <algorithm>
 #include <cmath>
 
-#include "fold.hpp"
-#include "norm.hpp"
+#include "bucket_run.hpp"
 
 namespace ddpsim {
 namespace {
@@ -22,6 +21,18 @@ constexpr int kWaves = 4;    // waves of a workgroup
 constexpr int kFinishWaves = 16;     // waves of a block of the last join
 constexpr int64_t kWaveSlots = 512;  // sums of a parameter that one wave joins
 constexpr int kJoinGroup = kNormJoinGroup;
+constexpr int kSmallWaves = 16;      // waves of the one-workgroup kernels
+#ifndef DDPSIM_SMALL_NORM_TILES
+#define DDPSIM_SMALL_NORM_TILES 256
+#endif
+#ifndef DDPSIM_SMALL_SYNC_TILES
+#define DDPSIM_SMALL_SYNC_TILES 16
+#endif
+#ifndef DDPSIM_INLINE_TILES
+#define DDPSIM_INLINE_TILES 1024
+#endif
+constexpr int kSmallNormTiles = DDPSIM_SMALL_NORM_TILES;
+constexpr int kSmallSyncTiles = DDPSIM_SMALL_SYNC_TILES;
 static_assert(kGroup <= 64 && kGroup % kBatch == 0, "a lane per tile");
 static_assert(kBucketThreads == 64 && kBucketVpt == 1, "a plan tile is one vector per lane");
 
@@ -74,21 +85,19 @@ __device__ __forceinline__ uint64_t read_lane(uint64_t v, int lane) {
   return (static_cast<uint64_t>(hi) << 32) | lo;
 }
 
+// The partial sums of one wave: group g of `group` tiles (at most kGroup) of
+// the rank whose addresses are `grads`, to out[g + descriptor index].
 template <typename Tr, int NT>
-__global__ __launch_bounds__(64 * kWaves) void grad_norm_kernel(
-    const SegDesc *__restrict__ seg, const int32_t *__restrict__ tile_seg, int64_t map_stride,
-    int64_t tiles, int64_t groups, int32_t n_params, const void *const *__restrict__ ptrs,
-    double *__restrict__ partial, int64_t slots) {
+__device__ __forceinline__ void norm_group(const SegDesc *__restrict__ seg,
+                                           const int32_t *__restrict__ tile_seg,
+                                           int64_t map_stride, int64_t tiles, int64_t g,
+                                           int32_t group, const void *const *__restrict__ grads,
+                                           double *out) {
   constexpr int V = Tr::kVec;
   const int lane = static_cast<int>(threadIdx.x) & 63;
-  const int64_t g = int64_t(blockIdx.x) * kWaves +
-                    __builtin_amdgcn_readfirstlane(static_cast<int32_t>(threadIdx.x) >> 6);
-  if (g >= groups) return;
-  const int32_t rank = static_cast<int32_t>(blockIdx.y);
-  const LaneTile mine = lane_tile<Tr>(seg, tile_seg, map_stride, g * kGroup + lane, tiles,
-                                      ptrs + static_cast<int64_t>(rank) * n_params,
-                                      lane < kGroup);
-  double *out = partial + static_cast<int64_t>(rank) * slots + g;
+  const LaneTile mine = lane_tile<Tr>(seg, tile_seg, map_stride, g * group + lane, tiles, grads,
+                                      lane < group);
+  out += g;
   // a lane adds the odd elements at its tile's parameter's ends
   NormSum<NT> odd;
   for (int i = 0; i < mine.n_head; ++i) {
@@ -112,7 +121,7 @@ __global__ __launch_bounds__(64 * kWaves) void grad_norm_kernel(
     for (int u = 0; u < kBatch; ++u) {
       const uint64_t src = read_lane(mine.src, b + u);
       const int32_t count = __builtin_amdgcn_readlane(mine.count, b + u);
-      x[u] = lane < count ? load_vec(reinterpret_cast<const void *>(src), lane)
+      x[u] = lane < count ? load_vec<true>(reinterpret_cast<const void *>(src), lane)
                           : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
@@ -130,9 +139,23 @@ __global__ __launch_bounds__(64 * kWaves) void grad_norm_kernel(
   }
   flush();
   // the group's last tile, and the slot after it if its parameter ends there
-  const int64_t left = tiles - g * kGroup;
-  const int32_t last = static_cast<int32_t>(left < kGroup ? left : kGroup) - 1;
+  const int64_t left = tiles - g * group;
+  const int32_t last = static_cast<int32_t>(left < group ? left : group) - 1;
   if (lane == last && mine.ends) out[cur + 1] = 0.0;
+}
+
+template <typename Tr, int NT>
+__global__ __launch_bounds__(64 * kWaves) void grad_norm_kernel(
+    const SegDesc *__restrict__ seg, const int32_t *__restrict__ tile_seg, int64_t map_stride,
+    int64_t tiles, int64_t groups, int32_t n_params, const void *const *__restrict__ ptrs,
+    double *__restrict__ partial, int64_t slots) {
+  const int64_t g = int64_t(blockIdx.x) * kWaves +
+                    __builtin_amdgcn_readfirstlane(static_cast<int32_t>(threadIdx.x) >> 6);
+  if (g >= groups) return;
+  const int32_t rank = static_cast<int32_t>(blockIdx.y);
+  norm_group<Tr, NT>(seg, tile_seg, map_stride, tiles, g, kGroup,
+                     ptrs + static_cast<int64_t>(rank) * n_params,
+                     partial + static_cast<int64_t>(rank) * slots);
 }
 
 // The tile sums of a large plan, joined in groups of kJoinGroup tiles before
@@ -186,10 +209,18 @@ __device__ __forceinline__ NormSum<NT> join_range(const double *__restrict__ par
   return sum;
 }
 
+// The partial sums [i0, i1) of descriptor i, with `group` tiles per sum (1: a
+// sum per tile, without gaps).
+__device__ __forceinline__ void slots_of_param(const SegDesc &d, int32_t i, int32_t group,
+                                               int64_t tile_elems, int64_t &i0, int64_t &i1) {
+  const int64_t a = d.tile_begin, b = a + (d.len + tile_elems - 1) / tile_elems;
+  i0 = group == 1 ? a : a / group + i;
+  i1 = group == 1 ? b : (b - 1) / group + i + 1;
+}
+
 // Block 0 joins all of a rank's partial sums into its norm; the other blocks
 // take kFinishWaves descriptors each and join those of each parameter, a wave
 // per parameter, or the whole block for one of more than kWaveSlots sums.
-// `group` is the tiles per partial sum (1: a sum per tile, without gaps).
 template <int NT>
 __global__ __launch_bounds__(64 * kFinishWaves) void norm_finish_kernel(
     const double *__restrict__ partial, int64_t slots, const SegDesc *__restrict__ seg,
@@ -218,9 +249,7 @@ __global__ __launch_bounds__(64 * kFinishWaves) void norm_finish_kernel(
   const int32_t s0 = (static_cast<int32_t>(blockIdx.x) - 1) * kFinishWaves;
   const auto range_of = [&](int32_t i, int64_t &i0, int64_t &i1) {
     const SegDesc d = seg[i];
-    const int64_t a = d.tile_begin, b = a + (d.len + tile_elems - 1) / tile_elems;
-    i0 = group == 1 ? a : a / group + i;
-    i1 = group == 1 ? b : (b - 1) / group + i + 1;
+    slots_of_param(d, i, group, tile_elems, i0, i1);
     return param_norms + static_cast<int64_t>(rank) * n_params + d.param;
   };
   __shared__ int32_t large[kFinishWaves];
@@ -243,19 +272,142 @@ __global__ __launch_bounds__(64 * kFinishWaves) void norm_finish_kernel(
   }
 }
 
+// A rank's norms from sums in LDS, by one workgroup of kSmallWaves waves that
+// all have passed a barrier since the sums were written: wave 0 the norm
+// (returned to every wave), all of them the parameters'.
+template <int NT>
+__device__ __forceinline__ float finish_in_lds(const double *sums, int64_t slots,
+                                               const SegDesc *__restrict__ seg, int32_t nseg,
+                                               int32_t group, int64_t tile_elems,
+                                               int32_t n_params, float *norm,
+                                               float *param_norms) {
+  const int lane = static_cast<int>(threadIdx.x) & 63;
+  const int wave = static_cast<int>(threadIdx.x) >> 6;
+  NormSum<NT> all;
+  for (int64_t i = lane; i < slots; i += 64) all.join_part(sums[i]);
+  join_wave(all);
+  if (threadIdx.x == 0) *norm = all.norm();
+  if (param_norms != nullptr) {
+    for (int32_t s = wave; s < nseg; s += kSmallWaves) {
+      const SegDesc d = seg[s];
+      int64_t i0, i1;
+      slots_of_param(d, s, group, tile_elems, i0, i1);
+      NormSum<NT> sum;
+      for (int64_t i = i0 + lane; i < i1; i += 64) sum.join_part(sums[i]);
+      join_wave(sum);
+      if (lane == 0) param_norms[d.param] = sum.norm();
+    }
+  }
+  return all.norm();
+}
+
+// Parameters without elements have no descriptor: their norms, before the
+// others' (a barrier lies between).
+__device__ __forceinline__ void zero_norms(float *param_norms, int32_t nseg, int32_t n_params) {
+  if (param_norms == nullptr || nseg == n_params) return;
+  for (int32_t i = static_cast<int32_t>(threadIdx.x); i < n_params; i += 64 * kSmallWaves) {
+    param_norms[i] = 0.0f;
+  }
+}
+
+// The norms of a small set in one launch, a workgroup per rank: no sum leaves
+// it, so that nothing waits for a second kernel.
+template <typename Tr, int NT>
+__global__ __launch_bounds__(64 * kSmallWaves) void small_norm_kernel(
+    const SegDesc *__restrict__ seg, const int32_t *__restrict__ tile_seg, int64_t map_stride,
+    int32_t tiles, int32_t nseg, int32_t n_params, const void *const *__restrict__ ptrs,
+    float *__restrict__ norms, float *__restrict__ param_norms) {
+  __shared__ double sums[kSmallNormTiles / 2 + kSmallNormTiles + 1];
+  const int32_t rank = static_cast<int32_t>(blockIdx.x);
+  const int64_t first = static_cast<int64_t>(rank) * n_params;
+  if (param_norms != nullptr) param_norms += first;
+  zero_norms(param_norms, nseg, n_params);
+  // groups of equal work for the waves, but of two tiles at least: slots of
+  // single tiles would be those of tile sums
+  const int32_t group =
+      std::max(2, std::min(kGroup, (tiles + kSmallWaves - 1) / kSmallWaves));
+  const int32_t groups = (tiles + group - 1) / group;
+  const int32_t wave = __builtin_amdgcn_readfirstlane(static_cast<int32_t>(threadIdx.x) >> 6);
+  for (int32_t g = wave; g < groups; g += kSmallWaves) {
+    norm_group<Tr, NT>(seg, tile_seg, map_stride, tiles, g, group, ptrs + first, sums);
+  }
+  __syncthreads();
+  finish_in_lds<NT>(sums, groups + nseg, seg, nseg, group, 64 * Tr::kVec, n_params, norms + rank,
+                    param_norms);
+}
+
+// All-reduce, norm and clip of a small set (a tile per wave) by one workgroup,
+// in one launch: the averages are staged as kStageNorm does, and spread by
+// the waves that folded them.
+template <typename Tr, int NT>
+__global__ __launch_bounds__(64 * kSmallWaves) void small_sync_kernel(
+    const SegDesc *__restrict__ seg, const int32_t *__restrict__ tile_seg, int64_t map_stride,
+    int32_t tiles, int32_t nseg, int32_t n_params, const void *const *__restrict__ ptrs,
+    int32_t p, Divide div, float max_norm, float eps, float *__restrict__ norm,
+    float *__restrict__ param_norms) {
+  __shared__ double sums[kSmallSyncTiles];
+  constexpr int64_t kTile = 64 * Tr::kVec;
+  const int32_t wave = __builtin_amdgcn_readfirstlane(static_cast<int32_t>(threadIdx.x) >> 6);
+  zero_norms(param_norms, nseg, n_params);
+  for (int32_t tile = wave; tile < tiles; tile += kSmallWaves) {
+    const SegDesc d = seg[tile_seg[tile_map_index(tile, map_stride)]];
+    const int64_t t = tile - d.tile_begin;
+    Epilogue<kStageNorm, NT> epi;
+    bucket_run<Tr, 1, 8>(d, t, t + 1, tile, n_params, ptrs, p, div, epi);
+    join_wave(epi.sum);
+    if ((threadIdx.x & 63) == 0) sums[tile] = epi.sum.part();
+  }
+  __syncthreads();
+  const float c = clip_coefficient(
+      finish_in_lds<NT>(sums, tiles, seg, nseg, 1, kTile, n_params, norm, param_norms), max_norm,
+      eps);
+  for (int32_t tile = wave; tile < tiles; tile += kSmallWaves) {
+    const SegDesc d = seg[tile_seg[tile_map_index(tile, map_stride)]];
+    spread_tile<Tr, true, false>(d, tile, n_params, ptrs, p, 0, p, c, false);
+  }
+}
+
 __global__ void zero_floats_kernel(float *p, int64_t n) {
   const int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
   if (i < n) p[i] = 0.0f;
 }
 
+template <typename Tr, bool kNt>
+__device__ __forceinline__ void clip_tiles(const LaneTile &mine, int lane, float c) {
+  constexpr int V = Tr::kVec;
+#pragma unroll
+  for (int b = 0; b < kGroup; b += kBatch) {
+    uint4 x[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const uint64_t src = read_lane(mine.src, b + u);
+      const int32_t count = __builtin_amdgcn_readlane(mine.count, b + u);
+      x[u] = lane < count ? load_vec<kNt>(reinterpret_cast<const void *>(src), lane)
+                          : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const uint64_t dst = read_lane(mine.src, b + u);
+      const int32_t count = __builtin_amdgcn_readlane(mine.count, b + u);
+      float w[V];
+      Tr::widen(x[u], w);
+#pragma unroll
+      for (int e = 0; e < V; ++e) w[e] = w[e] * c;
+      if (lane < count) store_vec<kNt>(reinterpret_cast<void *>(dst), lane, Tr::narrow(w));
+    }
+  }
+}
+
 // One wave per group of tiles of one rank: load, scale, store. A coefficient
-// of one changes no value, so such a rank's gradients are not touched.
+// of one changes no value, so such a rank's gradients are not touched. Whole
+// lines go past the caches when the gradients outgrow them, as in spread_tile
+// (GPT-2 small on 8 ranks, each by itself: 1.43 ms against 1.50 with ordinary
+// accesses; tiles inside lines: 0.18 ms ordinary, 0.23 past the caches).
 template <typename Tr>
 __global__ __launch_bounds__(64 * kWaves) void clip_kernel(
     const SegDesc *__restrict__ seg, const int32_t *__restrict__ tile_seg, int64_t map_stride,
     int64_t tiles, int64_t groups, int32_t n_params, const void *const *__restrict__ ptrs,
-    const float *__restrict__ norms, int32_t norm_step, float max_norm, float eps) {
-  constexpr int V = Tr::kVec;
+    const float *__restrict__ norms, int32_t norm_step, float max_norm, float eps, bool stream) {
   const int32_t rank = static_cast<int32_t>(blockIdx.y);
   const float c = clip_coefficient(norms[rank * norm_step], max_norm, eps);
   if (c == 1.0f) return;
@@ -274,138 +426,55 @@ __global__ __launch_bounds__(64 * kWaves) void clip_kernel(
     void *at = reinterpret_cast<void *>(mine.tail);
     Tr::store1(at, i, Tr::load1(at, i) * c);
   }
-#pragma unroll
-  for (int b = 0; b < kGroup; b += kBatch) {
-    uint4 x[kBatch];
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const uint64_t src = read_lane(mine.src, b + u);
-      const int32_t count = __builtin_amdgcn_readlane(mine.count, b + u);
-      x[u] = lane < count ? load_vec(reinterpret_cast<const void *>(src), lane)
-                          : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const uint64_t dst = read_lane(mine.src, b + u);
-      const int32_t count = __builtin_amdgcn_readlane(mine.count, b + u);
-      float w[V];
-      Tr::widen(x[u], w);
-#pragma unroll
-      for (int e = 0; e < V; ++e) w[e] = w[e] * c;
-      if (lane < count) store_vec<false>(reinterpret_cast<void *>(dst), lane, Tr::narrow(w));
-    }
+  if (stream && __all(mine.count == 0 || mine.src % static_cast<uint64_t>(kLineBytes) == 0)) {
+    clip_tiles<Tr, true>(mine, lane, c);
+  } else {
+    clip_tiles<Tr, false>(mine, lane, c);
   }
 }
 
-// One source, p destinations: a workgroup takes a tile; each of its waves
-// loads it, scales it and writes it to its own share of the ranks
-// (fanout_waves). The source is rank 0 (kStaged false: replicated gradients)
-// or what kStageNorm left in the tile's staging rank. The source is among the
-// destinations: all waves have loaded before any stores. Ranks whose copies
-// of a parameter sit at different offsets from a 16-byte boundary take
-// elements.
-//
-// Tiles that start on a cache line are stored past the caches when the
-// gradients outgrow them (`stream`): GPT-2 small on 8 ranks 0.72 ms against
-// 0.81 with ordinary stores. A tile that starts inside a line leaves lines to
-// two workgroups, whose halves an L2 has to put together: ordinary stores,
-// and neighbouring tiles on one XCD (xcd_run), take 0.94 ms instead of 1.07
-// for 300 odd tensors of that size, and 0.13 instead of 0.21 for 300 on 64
-// ranks.
+// The norm of at most kInlineTiles tile sums, by every wave for itself.
+constexpr int kInlineTiles = DDPSIM_INLINE_TILES;
+template <int NT>
+__device__ __forceinline__ float wave_norm(const double *__restrict__ partial, int32_t n) {
+  NormSum<NT> sum = join_range<NT>(partial, 0, n, static_cast<int>(threadIdx.x) & 63, 64);
+  join_wave(sum);
+  return sum.norm();
+}
+
+// What the spreading pass scales by: a norm in memory, or (sums > 0) the
+// pass's own join of that many tile sums, which one wave writes down. Up to
+// kInlineTiles sums that costs less than one more launch.
+struct NormSource {
+  float *norm;
+  const double *partial;
+  int32_t sums;
+  int32_t norm_type;
+};
+__device__ __forceinline__ float read_norm(const NormSource &src) {
+  if (src.sums == 0) return *src.norm;
+  const float n = src.norm_type == DDP_NORM_L2   ? wave_norm<DDP_NORM_L2>(src.partial, src.sums)
+                  : src.norm_type == DDP_NORM_L1 ? wave_norm<DDP_NORM_L1>(src.partial, src.sums)
+                                                 : wave_norm<DDP_NORM_INF>(src.partial, src.sums);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *src.norm = n;
+  return n;
+}
+
+// A workgroup takes a tile; its waves split the ranks (fanout_waves).
 template <typename Tr, bool kStaged>
 __global__ __launch_bounds__(64 * kMaxFanoutWaves) void clip_fanout_kernel(
     const SegDesc *__restrict__ seg, const int32_t *__restrict__ tile_seg, int64_t map_stride,
     int64_t tiles, int32_t n_params, const void *const *__restrict__ ptrs, int32_t p,
-    const float *__restrict__ norms, float max_norm, float eps, bool stream, bool runs) {
-  constexpr int V = Tr::kVec;
-  constexpr int64_t kElemBytes = sizeof(typename Tr::elem);
-  constexpr int64_t kTile = 64 * V;
-  const float c = clip_coefficient(norms[0], max_norm, eps);
+    NormSource source, float max_norm, float eps, bool stream, bool runs) {
+  const float c = clip_coefficient(read_norm(source), max_norm, eps);
   if (!kStaged && c == 1.0f) return;
-  const int lane = static_cast<int>(threadIdx.x) & 63;
   const int32_t waves = static_cast<int32_t>(blockDim.x) / 64;
   const int32_t wave = __builtin_amdgcn_readfirstlane(static_cast<int32_t>(threadIdx.x) >> 6);
-  const int32_t k0 = wave * p / waves, k1 = (wave + 1) * p / waves;
-  for (int64_t w0 = blockIdx.x; w0 < tiles; w0 += gridDim.x) {
-    const int64_t tile = runs ? xcd_run<kXcdRun>(w0, tiles) : w0;
+  for (int64_t w = blockIdx.x; w < tiles; w += gridDim.x) {
+    const int64_t tile = runs ? xcd_run<kXcdRun>(w, tiles) : w;
     const SegDesc d = seg[tile_seg[tile_map_index(tile, map_stride)]];
-    const int64_t t = tile - d.tile_begin;
-    const int32_t a = kStaged ? stage_rank(p, static_cast<int32_t>(tile)) : 0;
-    const int32_t b = ring_rank(a, 1, p);
-    const int32_t rot = store_rotation(p, static_cast<uint32_t>(tile));
-    const uint64_t mine =
-        lane < p ? reinterpret_cast<uint64_t>(ptrs[static_cast<int64_t>(lane) * n_params + d.param])
-                 : 0;
-    const uint64_t phase = __builtin_amdgcn_readlane(static_cast<uint32_t>(mine), 0) %
-                           static_cast<uint32_t>(kVecBytes);
-    const bool same = __all(lane >= p || mine % kVecBytes == phase);
-    const int64_t m = same ? static_cast<int64_t>(phase) / kElemBytes : 0;
-    const GradPtrs at{ptrs, n_params, d.param, m * kElemBytes};
-    const LanePtrs lat{mine - static_cast<uint64_t>(m * kElemBytes)};
-    auto load1 = [&](int64_t i) {
-      return kStaged ? Tr::unstage1(at(a), at(b), i) : Tr::load1(at(0), i);
-    };
-    if (!same) {  // the same for every wave
-      for (int64_t i = t * kTile + lane; i < (t + 1) * kTile; i += 64) {
-        const bool in = i < d.len;
-        float y = in ? load1(i) * c : 0.0f;
-        asm volatile("" : "+v"(y));
-        __syncthreads();
-        for (int32_t r = k0; in && r < k1; ++r) Tr::store1(at(r), i, y);
-      }
-      continue;
-    }
-    // this lane's vector, and on a parameter's first tile an odd element
-    const ChunkSpan k = make_span(m, d.len + m, V);
-    const int64_t v0 = k.vs / V + t * 64;
-    const int64_t v = v0 + lane;
-    const bool ok = v < k.ve / V;
-    uint4 x = make_uint4(0, 0, 0, 0), x2 = x;
-    if (ok) {
-      x = load_vec(lat(a), v);
-      if constexpr (kStaged && Tr::kStageRanks == 2) x2 = load_vec(lat(b), v);
-    }
-    int64_t J = 0;
-    bool odd = false;
-    float y1 = 0.0f;
-    if (t == 0 && lane >= 64 - 2 * (V - 1)) {
-      const int i = lane - (64 - 2 * (V - 1));
-      const bool head = i < V - 1;
-      J = head ? k.s + i : k.tail_begin + (i - (V - 1));
-      odd = J < (head ? k.head_end : k.e);
-      if (odd) y1 = load1(J) * c;
-    }
-    float f[V];
-    if constexpr (kStaged) {
-      Tr::unsplit(x, x2, f);
-    } else {
-      Tr::widen(x, f);
-    }
-#pragma unroll
-    for (int e = 0; e < V; ++e) f[e] = f[e] * c;
-    uint4 y = Tr::narrow(f);
-    // what is stored has been computed, so every load has returned, before
-    // the barrier that lets the other waves overwrite the source
-    asm volatile("" : "+v"(y.x), "+v"(y.y), "+v"(y.z), "+v"(y.w), "+v"(y1));
-    __syncthreads();
-    const bool lines =
-        stream && __all(lane >= p || (lat.mine + static_cast<uint64_t>(v0) * kVecBytes) %
-                                             static_cast<uint64_t>(kLineBytes) == 0);
-    // two loops: one loop with two kinds of store would be given one kind
-    if (lines) {
-      for (int32_t r = k0; r < k1; ++r) {
-        void *dst = lat(ring_rank(rot, r, p));
-        if (ok) store_vec<true>(dst, v, y);
-      }
-    } else {
-      for (int32_t r = k0; r < k1; ++r) {
-        void *dst = lat(ring_rank(rot, r, p));
-        if (ok) store_vec<false>(dst, v, y);
-      }
-    }
-    if (odd) {
-      for (int32_t r = k0; r < k1; ++r) Tr::store1(at(ring_rank(rot, r, p)), J, y1);
-    }
+    spread_tile<Tr, kStaged, true>(d, tile, n_params, ptrs, p, wave * p / waves,
+                                   (wave + 1) * p / waves, c, stream);
   }
 }
 
@@ -517,49 +586,95 @@ ddp_status launch_tile_finish(const PlanTiles &t, int32_t norm_type, double *par
   }
 }
 
-ddp_status launch_finish(const PlanTiles &t, int32_t norm_type, const double *partial,
-                         int64_t slots, int32_t group, int32_t ranks, float *d_norms,
-                         float *d_param_norms, hipStream_t stream, CallTimer &timer, bool last) {
+template <typename Tr, int NT>
+ddp_status launch_small_norm(const PlanTiles &t, int32_t p, const void *const *ptrs,
+                             float *d_norms, float *d_param_norms, hipStream_t stream,
+                             CallTimer &timer, bool last) {
+  return launch(small_norm_kernel<Tr, NT>, dim3(static_cast<uint32_t>(p)), dim3(64 * kSmallWaves),
+                stream, timer, last, "small_norm_kernel launch", t.seg, t.tile_seg, t.map_stride,
+                static_cast<int32_t>(t.tiles), t.nseg, t.n_params, ptrs, d_norms, d_param_norms);
+}
+
+template <typename Tr, int NT>
+ddp_status launch_small_sync(const PlanTiles &t, int32_t p, const void *const *ptrs,
+                             const Divide &div, float max_norm, float eps, float *d_norm,
+                             float *d_param_norms, hipStream_t stream, CallTimer &timer) {
+  return launch(small_sync_kernel<Tr, NT>, dim3(1), dim3(64 * kSmallWaves), stream, timer, true,
+                "small_sync_kernel launch", t.seg, t.tile_seg, t.map_stride,
+                static_cast<int32_t>(t.tiles), t.nseg, t.n_params, ptrs, p, div, max_norm, eps,
+                d_norm, d_param_norms);
+}
+
+template <typename Tr>
+ddp_status launch_small_sync_type(int32_t norm_type, const PlanTiles &t, int32_t p,
+                                  const void *const *ptrs, const Divide &div, float max_norm,
+                                  float eps, float *d_norm, float *d_param_norms,
+                                  hipStream_t stream, CallTimer &timer) {
   switch (norm_type) {
     case DDP_NORM_L2:
-      return launch_finish_nt<DDP_NORM_L2>(t, partial, slots, group, ranks, d_norms,
-                                           d_param_norms, stream, timer, last);
+      return launch_small_sync<Tr, DDP_NORM_L2>(t, p, ptrs, div, max_norm, eps, d_norm,
+                                                d_param_norms, stream, timer);
     case DDP_NORM_L1:
-      return launch_finish_nt<DDP_NORM_L1>(t, partial, slots, group, ranks, d_norms,
-                                           d_param_norms, stream, timer, last);
+      return launch_small_sync<Tr, DDP_NORM_L1>(t, p, ptrs, div, max_norm, eps, d_norm,
+                                                d_param_norms, stream, timer);
     default:
-      return launch_finish_nt<DDP_NORM_INF>(t, partial, slots, group, ranks, d_norms,
-                                            d_param_norms, stream, timer, last);
+      return launch_small_sync<Tr, DDP_NORM_INF>(t, p, ptrs, div, max_norm, eps, d_norm,
+                                                 d_param_norms, stream, timer);
   }
 }
 
 template <typename Tr, int NT>
 ddp_status launch_norm(const PlanTiles &t, int32_t p, const void *const *ptrs, double *partial,
-                       int64_t slots, hipStream_t stream, CallTimer &timer) {
-  const int64_t groups = norm_groups(t);
-  return launch(grad_norm_kernel<Tr, NT>,
-                dim3(static_cast<uint32_t>(ceil_div(groups, kWaves)), static_cast<uint32_t>(p)),
-                dim3(64 * kWaves), stream, timer, false, "grad_norm_kernel launch", t.seg,
-                t.tile_seg, t.map_stride, t.tiles, groups, t.n_params, ptrs, partial, slots);
+                       float *d_norms, float *d_param_norms, hipStream_t stream,
+                       CallTimer &timer, bool last) {
+  if (t.tiles > 0 && t.tiles <= kSmallNormTiles) {
+    return launch_small_norm<Tr, NT>(t, p, ptrs, d_norms, d_param_norms, stream, timer, last);
+  }
+  const int64_t slots = norm_slots(t);
+  if (t.tiles > 0) {
+    const int64_t groups = norm_groups(t);
+    ddp_status s = launch(grad_norm_kernel<Tr, NT>,
+                          dim3(static_cast<uint32_t>(ceil_div(groups, kWaves)),
+                               static_cast<uint32_t>(p)),
+                          dim3(64 * kWaves), stream, timer, false, "grad_norm_kernel launch",
+                          t.seg, t.tile_seg, t.map_stride, t.tiles, groups, t.n_params, ptrs,
+                          partial, slots);
+    if (s != DDP_OK) return s;
+  }
+  return launch_finish_nt<NT>(t, partial, slots, kGroup, p, d_norms, d_param_norms, stream, timer,
+                              last);
 }
 
 template <typename Tr>
-ddp_status launch_norm_type(int32_t norm_type, const PlanTiles &t, int32_t p,
-                            const void *const *ptrs, double *partial, int64_t slots,
-                            hipStream_t stream, CallTimer &timer) {
+ddp_status launch_norm_of(int32_t norm_type, const PlanTiles &t, int32_t p,
+                          const void *const *ptrs, double *partial, float *d_norms,
+                          float *d_param_norms, hipStream_t stream, CallTimer &timer, bool last) {
   switch (norm_type) {
     case DDP_NORM_L2:
-      return launch_norm<Tr, DDP_NORM_L2>(t, p, ptrs, partial, slots, stream, timer);
+      return launch_norm<Tr, DDP_NORM_L2>(t, p, ptrs, partial, d_norms, d_param_norms, stream,
+                                          timer, last);
     case DDP_NORM_L1:
-      return launch_norm<Tr, DDP_NORM_L1>(t, p, ptrs, partial, slots, stream, timer);
+      return launch_norm<Tr, DDP_NORM_L1>(t, p, ptrs, partial, d_norms, d_param_norms, stream,
+                                          timer, last);
     default:
-      return launch_norm<Tr, DDP_NORM_INF>(t, p, ptrs, partial, slots, stream, timer);
+      return launch_norm<Tr, DDP_NORM_INF>(t, p, ptrs, partial, d_norms, d_param_norms, stream,
+                                           timer, last);
   }
+}
+
+ddp_status launch_norm_type(int32_t dtype, int32_t norm_type, const PlanTiles &t, int32_t p,
+                            const void *const *ptrs, double *partial, float *d_norms,
+                            float *d_param_norms, hipStream_t stream, CallTimer &timer,
+                            bool last) {
+  return dtype == DDP_F32 ? launch_norm_of<F32Traits>(norm_type, t, p, ptrs, partial, d_norms,
+                                                      d_param_norms, stream, timer, last)
+                          : launch_norm_of<BF16Traits>(norm_type, t, p, ptrs, partial, d_norms,
+                                                       d_param_norms, stream, timer, last);
 }
 
 template <typename Tr, bool kStaged>
 ddp_status launch_fanout(const PlanTiles &t, int32_t p, const void *const *ptrs,
-                         const float *d_norms, float max_norm, float eps, hipStream_t stream,
+                         const NormSource &source, float max_norm, float eps, hipStream_t stream,
                          CallTimer &timer) {
   const int32_t waves = fanout_waves(p);
   // a launch holds at most 2^32 - 1 work-items along x
@@ -568,22 +683,40 @@ ddp_status launch_fanout(const PlanTiles &t, int32_t p, const void *const *ptrs,
   return launch(clip_fanout_kernel<Tr, kStaged>, dim3(static_cast<uint32_t>(blocks)),
                 dim3(static_cast<uint32_t>(64 * waves)), stream, timer, true,
                 "clip_fanout_kernel launch", t.seg, t.tile_seg, t.map_stride, t.tiles, t.n_params,
-                ptrs, p, d_norms, max_norm, eps, past_cache, runs_per_xcd(t, p));
+                ptrs, p, source, max_norm, eps, past_cache, runs_per_xcd(t, p));
 }
 
 template <typename Tr>
-ddp_status launch_clip(const PlanTiles &t, int32_t p, const void *const *ptrs,
-                       const float *d_norms, int32_t n_norms, float max_norm, float eps,
-                       bool replicated, hipStream_t stream, CallTimer &timer) {
+ddp_status launch_clip_of(const PlanTiles &t, int32_t p, const void *const *ptrs,
+                          const float *d_norms, int32_t n_norms, float max_norm, float eps,
+                          bool replicated, hipStream_t stream, CallTimer &timer) {
   if (replicated && p > 1) {
-    return launch_fanout<Tr, false>(t, p, ptrs, d_norms, max_norm, eps, stream, timer);
+    const NormSource source = {const_cast<float *>(d_norms), nullptr, 0, 0};
+    return launch_fanout<Tr, false>(t, p, ptrs, source, max_norm, eps, stream, timer);
   }
   const int64_t groups = norm_groups(t);
-  return launch(clip_kernel<Tr>,
-                dim3(static_cast<uint32_t>(ceil_div(groups, kWaves)), static_cast<uint32_t>(p)),
-                dim3(64 * kWaves), stream, timer, true, "clip_kernel launch", t.seg, t.tile_seg,
-                t.map_stride, t.tiles, groups, t.n_params, ptrs, d_norms,
-                n_norms == 1 ? 0 : 1, max_norm, eps);
+  const bool past_cache = int64_t(p) * t.elems * t.elem_bytes > kCacheBytes;
+  // Past the caches a full CU of waves, each with a stream in and one out,
+  // opens more DRAM rows than pay: GPT-2 small on 8 ranks 1.36 ms, with 2
+  // workgroups per CU 1.28, with 4 1.33; tensors that are not whole lines
+  // prefer 4 (100 odd bf16 tensors on 4 ranks 0.39 ms, unbounded 0.42, with 2
+  // 0.48).
+  const size_t lds = past_cache ? residency_lds(t.whole_lines ? 2 : 4) : 0;
+  return launch_lds(clip_kernel<Tr>,
+                    dim3(static_cast<uint32_t>(ceil_div(groups, kWaves)),
+                         static_cast<uint32_t>(p)),
+                    dim3(64 * kWaves), lds, stream, timer, true,
+                    "clip_kernel launch", t.seg, t.tile_seg, t.map_stride, t.tiles, groups,
+                    t.n_params, ptrs, d_norms, n_norms == 1 ? 0 : 1, max_norm, eps, past_cache);
+}
+
+ddp_status launch_clip(int32_t dtype, const PlanTiles &t, int32_t p, const void *const *ptrs,
+                       const float *d_norms, int32_t n_norms, float max_norm, float eps,
+                       bool replicated, hipStream_t stream, CallTimer &timer) {
+  return dtype == DDP_F32 ? launch_clip_of<F32Traits>(t, p, ptrs, d_norms, n_norms, max_norm, eps,
+                                                      replicated, stream, timer)
+                          : launch_clip_of<BF16Traits>(t, p, ptrs, d_norms, n_norms, max_norm,
+                                                       eps, replicated, stream, timer);
 }
 
 }  // namespace
@@ -607,18 +740,8 @@ extern "C" ddp_status ddp_grad_norm(const ddp_plan *plan, int32_t p,
     s = check_scratch(what, workspace, workspace_bytes, ddp_grad_norm_workspace(plan, p));
   }
   if (s != DDP_OK) return s;
-  double *partial = static_cast<double *>(workspace);
-  const int64_t slots = norm_slots(t);
-  if (t.tiles > 0) {
-    s = dtype == DDP_F32
-            ? launch_norm_type<F32Traits>(norm_type, t, p, d_grad_ptrs, partial, slots, stream,
-                                          timer)
-            : launch_norm_type<BF16Traits>(norm_type, t, p, d_grad_ptrs, partial, slots, stream,
-                                           timer);
-    if (s != DDP_OK) return s;
-  }
-  return launch_finish(t, norm_type, partial, slots, kGroup, p, d_norms, d_param_norms, stream,
-                       timer, true);
+  return launch_norm_type(dtype, norm_type, t, p, d_grad_ptrs, static_cast<double *>(workspace),
+                          d_norms, d_param_norms, stream, timer, true);
 }
 
 extern "C" ddp_status ddp_clip_grads(const ddp_plan *plan, int32_t p, void *const *d_grad_ptrs,
@@ -641,12 +764,8 @@ extern "C" ddp_status ddp_clip_grads(const ddp_plan *plan, int32_t p, void *cons
                 replicated ? " for replicated gradients" : ", or one per rank");
   }
   if (t.tiles == 0) return DDP_OK;
-  if (dtype == DDP_F32) {
-    return launch_clip<F32Traits>(t, p, d_grad_ptrs, d_norms, n_norms, max_norm, eps,
-                                  replicated != 0, stream, timer);
-  }
-  return launch_clip<BF16Traits>(t, p, d_grad_ptrs, d_norms, n_norms, max_norm, eps,
-                                 replicated != 0, stream, timer);
+  return launch_clip(dtype, t, p, d_grad_ptrs, d_norms, n_norms, max_norm, eps, replicated != 0,
+                     stream, timer);
 }
 
 extern "C" ddp_status ddp_allreduce_buckets_norm(const ddp_plan *plan, int32_t first_bucket,
@@ -723,31 +842,52 @@ extern "C" ddp_status ddp_allreduce_clip(const ddp_plan *plan, int32_t p,
   // against 1.50 at p = 8; bf16 0.48 against 0.41 at p = 2); a single rank
   // has no sum to keep.
   const bool staged = p > 1;
-  SyncEpilogue epi = {staged ? kStageNorm : kFoldNorm, norm_type, static_cast<double *>(workspace), d_norm, max_norm, eps,
-                      runs_per_xcd(t, p)};
   const int32_t nb = ddp_plan_num_buckets(plan);
-  if (stats != nullptr) *stats = ddp_comm_stats{};
-  if (nb > 0) {
-    s = allreduce_buckets(plan, 0, nb, p, d_grad_ptrs, dtype, avg_mode, tokens, stream, stats,
-                          DDPSIM_BUCKET_MAX_WORKGROUPS, &epi, &timer, false);
+  ddp_comm_stats local;
+  if (stats == nullptr) stats = &local;
+  *stats = ddp_comm_stats{};
+  double *sums = static_cast<double *>(workspace);
+  if (p == 1 && div.mode == kNone && t.tiles > 0) {
+    // one rank's gradients are their own average
+    s = launch_norm_type(dtype, norm_type, t, 1, d_grad_ptrs, sums, d_norm, d_param_norms, stream,
+                         timer, false);
     if (s != DDP_OK) return s;
+    s = launch_clip(dtype, t, 1, d_grad_ptrs, d_norm, 1, max_norm, eps, false, stream, timer);
+  } else if (staged && t.tiles > 0 && t.tiles <= kSmallSyncTiles) {
+    for (int32_t b = 0; b < nb; ++b) add_ring_stats(p, ddp_plan_bucket_numel(plan, b), stats);
+    s = dtype == DDP_F32
+            ? launch_small_sync_type<F32Traits>(norm_type, t, p, d_grad_ptrs, div, max_norm, eps,
+                                                d_norm, d_param_norms, stream, timer)
+            : launch_small_sync_type<BF16Traits>(norm_type, t, p, d_grad_ptrs, div, max_norm,
+                                                 eps, d_norm, d_param_norms, stream, timer);
+  } else {
+    SyncEpilogue epi = {staged ? kStageNorm : kFoldNorm, norm_type, sums, d_norm, max_norm, eps,
+                        runs_per_xcd(t, p)};
+    if (nb > 0) {
+      s = allreduce_buckets(plan, 0, nb, p, d_grad_ptrs, dtype, avg_mode, tokens, stream, stats,
+                            DDPSIM_BUCKET_MAX_WORKGROUPS, &epi, &timer, false);
+      if (s != DDP_OK) return s;
+    }
+    NormSource source = {d_norm, sums, 0, norm_type};
+    if (staged && t.tiles > 0 && t.tiles <= kInlineTiles && d_param_norms == nullptr) {
+      source.sums = static_cast<int32_t>(t.tiles);
+    } else {
+      s = launch_tile_finish(t, norm_type, sums, d_norm, d_param_norms, stream, timer,
+                             t.tiles == 0);
+      if (s != DDP_OK || t.tiles == 0) return s;
+    }
+    if (staged) {
+      s = dtype == DDP_F32 ? launch_fanout<F32Traits, true>(t, p, d_grad_ptrs, source, max_norm,
+                                                            eps, stream, timer)
+                           : launch_fanout<BF16Traits, true>(t, p, d_grad_ptrs, source, max_norm,
+                                                             eps, stream, timer);
+    } else {
+      epi.mode = kSyncScale;
+      s = allreduce_buckets(plan, 0, nb, p, d_grad_ptrs, dtype, avg_mode, tokens, stream, nullptr,
+                            DDPSIM_BUCKET_MAX_WORKGROUPS, &epi, &timer, true);
+    }
   }
-  s = launch_tile_finish(t, norm_type, epi.partial, d_norm, d_param_norms, stream, timer,
-                         t.tiles == 0);
-  if (s != DDP_OK || nb == 0) return s;
-  if (staged && t.tiles > 0) {
-    s = dtype == DDP_F32 ? launch_fanout<F32Traits, true>(t, p, d_grad_ptrs, d_norm, max_norm,
-                                                          eps, stream, timer)
-                         : launch_fanout<BF16Traits, true>(t, p, d_grad_ptrs, d_norm, max_norm,
-                                                           eps, stream, timer);
-  } else if (!staged) {
-    epi.mode = kSyncScale;
-    s = allreduce_buckets(plan, 0, nb, p, d_grad_ptrs, dtype, avg_mode, tokens, stream, nullptr,
-                          DDPSIM_BUCKET_MAX_WORKGROUPS, &epi, &timer, true);
-  }
-  if (stats != nullptr) {
-    const int64_t moved = staged ? 2 * p + (dtype == DDP_F32 ? 2 : 4) : 3 * p;
-    stats->hbm_bytes = moved * t.elems * t.elem_bytes;
-  }
+  const int64_t moved = staged ? 2 * p + (dtype == DDP_F32 ? 2 : 4) : 3 * p;
+  stats->hbm_bytes = moved * t.elems * t.elem_bytes;
   return s;
 }

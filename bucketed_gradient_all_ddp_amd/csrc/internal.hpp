@@ -268,6 +268,17 @@ ddp_status check_workspace(const char *what, const void *workspace, size_t works
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// One bucket's ring all-reduce of n elements added to `stats` (the logical
+// schedule; not the device traffic).
+inline void add_ring_stats(int32_t p, int64_t n, ddp_comm_stats *stats) {
+  const int64_t chunk = n > 0 ? ceil_div(n, p) : 0;
+  stats->steps += 2 * int64_t(p - 1);
+  stats->messages += 2 * int64_t(p) * (p - 1);
+  stats->bytes_sent_per_rank += 2 * int64_t(p - 1) * chunk * 4;
+  stats->bytes_recv_per_rank += 2 * int64_t(p - 1) * chunk * 4;
+  stats->total_bytes += 2 * int64_t(p) * (p - 1) * chunk * 4;
+}
+
 // Timing requested with ddp_time_next_call: the events are attached to the
 // first and the last kernel dispatch of the next entry-point call made on
 // this thread. take() moves the pending request into the call.
@@ -368,6 +379,7 @@ struct F32Traits {
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]),
                       __float_as_uint(f[2]), __float_as_uint(f[3]));
   }
+  __device__ static __forceinline__ float widen1(float x) { return x; }
   __device__ static __forceinline__ float load1(const void *base, int64_t i) {
     return global_ptr<float>(base)[i];
   }
@@ -406,6 +418,9 @@ struct BF16Traits {
   __device__ static __forceinline__ uint4 narrow(const float (&f)[8]) {
     return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
                       pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+  }
+  __device__ static __forceinline__ float widen1(uint16_t x) {
+    return __uint_as_float(static_cast<uint32_t>(x) << 16);
   }
   __device__ static __forceinline__ float load1(const void *base, int64_t i) {
     return __uint_as_float(

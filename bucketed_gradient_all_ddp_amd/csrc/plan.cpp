@@ -192,6 +192,7 @@ extern "C" size_t ddp_sync_norm_workspace(const ddp_plan *plan) {
   if (!plan_tiles(plan, &t)) return 0;
   int64_t sums = t.tiles;
   if (t.tiles > kNormJoinTiles) sums += ceil_div(t.tiles, kNormJoinGroup) + t.nseg;
+  sums = std::max(sums, norm_slots(t));  // a single rank's sums are ddp_grad_norm's
   return sizeof(double) * static_cast<size_t>(sums);
 }
 

@@ -34,7 +34,7 @@ def test_workspace_sizes():
         for p in (1, 3, 64):
             assert plan.grad_norm_workspace(p) == 8 * p * (-(-tiles // 16) + live)
         assert plan.grad_norm_workspace(0) == 0 and plan.grad_norm_workspace(65) == 0
-        assert plan.sync_norm_workspace() == 8 * tiles
+        assert plan.sync_norm_workspace() == 8 * max(tiles, -(-tiles // 16) + live)
     # past 32768 tiles: a second level of sums per 256 tiles and parameter
     assert ddp.ddp_bucket_plan([32768 * 256, 0], 4).sync_norm_workspace() == 8 * 32768
     big = ddp.ddp_bucket_plan([32768 * 256, 0, 1], 4)
