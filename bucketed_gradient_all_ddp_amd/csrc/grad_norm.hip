@@ -442,17 +442,18 @@ __device__ __forceinline__ float wave_norm(const double *__restrict__ partial, i
   return sum.norm();
 }
 
-// What the spreading pass scales by: a norm in memory, or (sums > 0) the
-// pass's own join of that many tile sums, which one wave writes down. Up to
-// kInlineTiles sums that costs less than one more launch.
+// What the spreading pass scales by: a norm in memory, or (kJoin) the pass's
+// own join of the tile sums, which one wave writes down. Up to kInlineTiles
+// sums that costs less than one more launch.
 struct NormSource {
   float *norm;
   const double *partial;
-  int32_t sums;
+  int32_t sums;  // 0: the norm is there
   int32_t norm_type;
 };
+template <bool kJoin>
 __device__ __forceinline__ float read_norm(const NormSource &src) {
-  if (src.sums == 0) return *src.norm;
+  if constexpr (!kJoin) return *src.norm;
   const float n = src.norm_type == DDP_NORM_L2   ? wave_norm<DDP_NORM_L2>(src.partial, src.sums)
                   : src.norm_type == DDP_NORM_L1 ? wave_norm<DDP_NORM_L1>(src.partial, src.sums)
                                                  : wave_norm<DDP_NORM_INF>(src.partial, src.sums);
@@ -461,12 +462,12 @@ __device__ __forceinline__ float read_norm(const NormSource &src) {
 }
 
 // A workgroup takes a tile; its waves split the ranks (fanout_waves).
-template <typename Tr, bool kStaged>
+template <typename Tr, bool kStaged, bool kJoin>
 __global__ __launch_bounds__(64 * kMaxFanoutWaves) void clip_fanout_kernel(
     const SegDesc *__restrict__ seg, const int32_t *__restrict__ tile_seg, int64_t map_stride,
     int64_t tiles, int32_t n_params, const void *const *__restrict__ ptrs, int32_t p,
     NormSource source, float max_norm, float eps, bool stream, bool runs) {
-  const float c = clip_coefficient(read_norm(source), max_norm, eps);
+  const float c = clip_coefficient(read_norm<kJoin>(source), max_norm, eps);
   if (!kStaged && c == 1.0f) return;
   const int32_t waves = static_cast<int32_t>(blockDim.x) / 64;
   const int32_t wave = __builtin_amdgcn_readfirstlane(static_cast<int32_t>(threadIdx.x) >> 6);
@@ -680,7 +681,11 @@ ddp_status launch_fanout(const PlanTiles &t, int32_t p, const void *const *ptrs,
   // a launch holds at most 2^32 - 1 work-items along x
   const int64_t blocks = std::min(t.tiles, int64_t(UINT32_MAX) / (64 * waves));
   const bool past_cache = int64_t(p) * t.elems * t.elem_bytes > kCacheBytes;
-  return launch(clip_fanout_kernel<Tr, kStaged>, dim3(static_cast<uint32_t>(blocks)),
+  auto kernel = clip_fanout_kernel<Tr, kStaged, false>;
+  if constexpr (kStaged) {
+    if (source.sums > 0) kernel = clip_fanout_kernel<Tr, true, true>;
+  }
+  return launch(kernel, dim3(static_cast<uint32_t>(blocks)),
                 dim3(static_cast<uint32_t>(64 * waves)), stream, timer, true,
                 "clip_fanout_kernel launch", t.seg, t.tile_seg, t.map_stride, t.tiles, t.n_params,
                 ptrs, p, source, max_norm, eps, past_cache, runs_per_xcd(t, p));
