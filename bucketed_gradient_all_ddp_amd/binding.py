@@ -773,6 +773,8 @@ def ddp_grad_norm_finish(plan: Plan, workspace, norm=None, norm_type: str = "l2"
     import torch
 
     what = "ddp_grad_norm_finish"
+    if workspace is None:
+        raise ValueError(f"{what}: needs the workspace the partial sums were left in")
     device = workspace.device
     with _on_device(workspace):
         if norm is None:

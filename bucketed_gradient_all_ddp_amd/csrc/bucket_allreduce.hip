@@ -377,7 +377,9 @@ ddp_status allreduce_buckets(const ddp_plan *plan, int32_t first_bucket, int32_t
   const void *const *grads = d_grad_ptrs;
   const WaveShape shape = epi == nullptr ? WaveShape{1, kBucketRb} : wave_shape(p, tiles, nseg);
   const int32_t units = (tiles - 1) / shape.tiles + 1;
-  const int32_t blocks = max_workgroups > 0 ? std::min(units, max_workgroups) : units;
+  // a launch holds at most 2^32 - 1 work-items along x
+  int32_t blocks = std::min(units, static_cast<int32_t>(UINT32_MAX / kBucketThreads));
+  if (max_workgroups > 0) blocks = std::min(blocks, max_workgroups);
   const dim3 grid(static_cast<uint32_t>(blocks));
   // Each workgroup keeps 2p streams of 1 KiB in flight (p loads, p
   // stores); a CU full of them (32 one-wave workgroups) puts more streams on

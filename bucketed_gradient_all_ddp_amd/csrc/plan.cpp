@@ -47,6 +47,7 @@ struct ddp_plan {
   size_t seg_bytes = 0;                   // the tile map starts here
   int64_t seg_map_stride = 0;             // entries per XCD group of the tile map
   void *d_seg = nullptr;
+  PlanTiles totals = {};  // what does not depend on an upload
 };
 
 namespace ddpsim {
@@ -111,20 +112,12 @@ bool plan_segment_info(const ddp_plan *plan, int32_t b, int32_t *first, int32_t 
 }
 
 bool plan_tiles(const ddp_plan *plan, PlanTiles *out) {
-  std::memset(out, 0, sizeof *out);
-  if (plan == nullptr) return false;
-  out->n_params = plan->n_params;
-  out->elem_bytes = plan->elem_bytes;
-  out->seg_p = plan->seg_p;
-  const int64_t tile_elems = bucket_tile_elems(kVecBytes / plan->elem_bytes);
-  out->whole_lines = true;
-  for (int64_t n : plan->numel) {
-    if (n == 0) continue;
-    if (n * plan->elem_bytes % kLineBytes != 0) out->whole_lines = false;
-    ++out->nseg;
-    out->tiles += ceil_div(n, tile_elems);
-    out->elems += n;
+  if (plan == nullptr) {
+    *out = PlanTiles{};
+    return false;
   }
+  *out = plan->totals;
+  out->seg_p = plan->seg_p;
   if (plan->seg_p != 0) {
     out->seg = static_cast<const SegDesc *>(plan->d_seg);
     out->tile_seg = plan_tile_map(plan, &out->map_stride);
@@ -353,6 +346,17 @@ ddp_status build_plan(const int64_t *numel, int32_t n_params, const int32_t *wal
       ++k;
     }
     plan->tiles.push_back(static_cast<int32_t>(tiles));
+  }
+  PlanTiles &sum = plan->totals;
+  sum.n_params = n_params;
+  sum.elem_bytes = elem_bytes;
+  sum.whole_lines = true;
+  for (int64_t n : plan->numel) {
+    if (n == 0) continue;
+    ++sum.nseg;
+    sum.elems += n;
+    sum.tiles += ceil_div(n, bucket_tile_elems(kVecBytes / elem_bytes));
+    if (n * elem_bytes % kLineBytes != 0) sum.whole_lines = false;
   }
   const size_t desc_bytes = plan->desc.size() * sizeof(ParamDesc);
   plan->staged.resize(desc_bytes + tile_desc.size() * sizeof(int32_t));

@@ -399,9 +399,13 @@ ddp_status ddp_grad_norm_finish(const ddp_plan *plan, int32_t norm_type,
 /* The all-reduce of every bucket, the norm of the averaged gradient and the
  * clip as one call: afterwards every rank's gradients hold c times the fp32
  * average (c as in ddp_clip_grads), rounded once to the gradients' type, and
- * *d_norm (and d_param_norms, if not NULL) the norm before clipping. In fp32
- * these are the bits of ddp_allreduce_buckets_norm, ddp_grad_norm_finish and
- * ddp_clip_grads one after another; in bf16 those round twice. The
+ * *d_norm (and d_param_norms, if not NULL) the norm before clipping. This is
+ * what ddp_allreduce_buckets_norm, ddp_grad_norm_finish and a replicated
+ * ddp_clip_grads leave one after another, but that those round bf16 twice
+ * (the norm's 64-bit sums may be joined in another order).
+ * Device traffic (2 p + 2) bytes-per-element in fp32 and 2 p + 4 in bf16: the
+ * averages wait for the norm in the memory of one rank's gradients (two
+ * ranks' for bf16), so that after a DDP_EHIP the gradients are undefined. The
  * descriptor table must be the one for p. The stats describe the ring
  * schedules, with the device traffic of this call. Errors: as
  * ddp_allreduce_buckets_norm and ddp_clip_grads. */

@@ -476,6 +476,64 @@ def test_reducer_with_norm_then_clip(oracle, bf16, cap):
     assert (ws == 255).all()
 
 
+@pytest.mark.parametrize("sizes", [
+    [4096 * 1024, 1024 * 1024, 4096, 16_384 * 1024, 32],        # whole cache lines
+    [4_000_003, 1_000_001, 77, 17_000_005, 1],                  # tiles inside lines
+])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_past_the_caches(sizes, bf16):
+    """Sets beyond the Infinity Cache, where stores, residency and the tiles'
+    order follow other rules. Small integers: averages of 8 and their squares
+    add up exactly in any order, so every value has one right answer."""
+    p, dt = 8, torch.bfloat16 if bf16 else torch.float32
+    stride = sum(sizes) + 64
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    arena = torch.randint(-8, 9, (p, stride), generator=g, device="cuda").to(dt)
+    assert arena.numel() * arena.element_size() > (256 << 20)
+    grads = [list(arena[r][:sum(sizes)].split(sizes)) for r in range(p)]
+    table = ddp.grad_pointer_table(grads)
+    plan = ddp.ddp_bucket_plan(sizes, 2 if bf16 else 4).upload_segments(p)
+    live = torch.zeros(stride, dtype=torch.bool, device="cuda")
+    live[:sum(sizes)] = True
+
+    def scales(norms, max_norm):
+        # (in numpy: torch divides a number by a tensor as reciprocal and
+        # product, two roundings)
+        return to_dev(np.array([_coefficient(n, max_norm, 1e-6) for n in to_host(norms)]))
+
+    # each rank clipped by its own norm
+    norms = ddp.ddp_grad_norm(plan, table, p)
+    exact = (arena.double() * live).square().sum(1).sqrt()
+    _close(to_host(norms), exact.cpu().numpy())
+    want = torch.where(live, arena.float() * scales(norms, 100.0)[:, None],
+                       arena.float()).to(dt)
+    keep = arena.clone()
+    ddp.ddp_clip_grads(plan, table, p, norms, 100.0)
+    assert torch.equal(arena, want)
+    # the sum of all ranks, clipped
+    arena.copy_(keep)
+    total = keep.float().sum(0) / p
+    ws, guard = _workspace(plan.sync_norm_workspace())
+    norm = torch.empty(1, device="cuda")
+    ddp.ddp_allreduce_clip(plan, table, p, 100.0, norm, ws, avg="world")
+    _close(to_host(norm), (total.double() * live).square().sum().sqrt().reshape(1).cpu().numpy())
+    got = (total * scales(norm, 100.0)).to(dt)
+    want = torch.where(live, got.expand(p, -1), keep)
+    assert torch.equal(arena, want)
+    assert (guard == 255).all()
+    # rank 0's spread to all, clipped again
+    ddp.ddp_clip_grads(plan, table, p, norm, 50.0, replicated=True)
+    got = (got.float() * scales(norm, 50.0)).to(dt)
+    assert torch.equal(arena, torch.where(live, got.expand(p, -1), keep))
+    # the averaging all-reduce with its norm
+    arena.copy_(keep)
+    ddp.ddp_allreduce_buckets_norm(plan, 0, plan.num_buckets, table, p, ws, avg="world")
+    again = ddp.ddp_grad_norm_finish(plan, ws)
+    _close(to_host(again), to_host(norm).astype(np.float64))
+    assert torch.equal(arena, torch.where(live, total.to(dt).expand(p, -1), keep))
+
+
 # ---------------------------------------------------------------------------
 # Streams, graphs, timing
 # ---------------------------------------------------------------------------
