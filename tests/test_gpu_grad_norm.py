@@ -27,6 +27,7 @@ SHAPES = {
     "one": [1],
     "tiny": [3, 1, 2],
     "none": [0, 0],
+    "holes": [0, 5, 0, 300, 0, 0, 1000],
     "group": [4096],
     "groups": [4096, 4096, 8192, 1],
     "small": [1] * 70 + [17] * 50,
