@@ -11,7 +11,6 @@ raises ImportError rather than falling back to anything else.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 import os
@@ -170,10 +169,18 @@ def _check(status: int, func: str) -> None:
         raise DDPError(status, func, detail)
 
 
+@functools.lru_cache(maxsize=None)
+def _torch():
+    """torch, imported on first use (the import statement in a function costs
+    a lookup per call, which small calls feel)."""
+    import torch
+
+    return torch
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-
+        torch = _torch()
         # the current stream's handle; torch.cuda.current_stream() builds a
         # Stream object around it, which costs as much as a kernel launch
         return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
@@ -527,10 +534,9 @@ def _check_grad_table(table, plan: "Plan", p: int, what: str) -> None:
     """The table must have been built by grad_pointer_table for p ranks of
     tensors shaped as the plan's parameters: the kernels read p * n_params
     addresses from it and write every element of every one."""
-    import torch
-
     if table is None:
         return  # the library refuses a NULL table wherever it would be read
+    torch = _torch()
     if not isinstance(table, torch.Tensor) or getattr(table, "_ddp_numel", None) is None:
         raise TypeError(f"{what}: build the gradient table with grad_pointer_table")
     if table.dtype != torch.int64 or not table.is_contiguous():
@@ -623,16 +629,10 @@ def ddp_allreduce_buckets(plan: Plan, first_bucket: int, n_buckets: int, grad_ta
 # Gradient norm and clipping
 # ---------------------------------------------------------------------------
 
-_SAME_DEVICE = contextlib.nullcontext()
-
-
-def _on_device(tensor):
-    """The library launches on the current device: make that the tensor's."""
-    import torch
-
-    if tensor is None or tensor.get_device() == torch._C._cuda_getDevice():
-        return _SAME_DEVICE
-    return torch.cuda.device(tensor.device)
+def _elsewhere(tensor) -> bool:
+    """Whether the tensor is on another device than the current one. The
+    library launches on the current device: calls make it the tensor's."""
+    return tensor is not None and tensor.get_device() != _torch()._C._cuda_getDevice()
 
 
 def _empty(n: int, dtype, device, stream):
@@ -667,9 +667,7 @@ def _floats(t, n: int, device, what: str, name: str) -> Optional[int]:
     """Address of a contiguous float32 device tensor of n elements."""
     if t is None:
         return None
-    import torch
-
-    if t.dtype is not torch.float32 or t.numel() != n or not t.is_contiguous():
+    if t.dtype is not _torch().float32 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{what}: {name} must be a contiguous float32 tensor of {n} elements")
     ptr = _device_ptr(t)
     if device is not None and t.get_device() != device.index:
@@ -701,28 +699,29 @@ def ddp_grad_norm(plan: Plan, grad_table, p: int, norms=None, norm_type: str = "
     = (first, count) takes some of the table's p ranks. `param_norms`, if
     given, is a float32 tensor [count, n_params] that receives every
     gradient's own norm."""
-    import torch
-
     what = "ddp_grad_norm"
     _check_grad_table(grad_table, plan, p, what)
+    if _elsewhere(grad_table):
+        with _torch().cuda.device(grad_table.device):
+            return ddp_grad_norm(plan, grad_table, p, norms, norm_type, param_norms, ranks,
+                                 workspace, stream)
     _check_norm_dtype(grad_table, what)
     first, count = (0, p) if ranks is None else ranks
     if first < 0 or count < 1 or first + count > p:
         raise ValueError(f"{what}: ranks {first}..{first + count - 1} outside 0..{p - 1}")
     device = grad_table.device if grad_table is not None else None
-    with _on_device(grad_table):
-        if norms is None:
-            norms = _empty(count, torch.float32, device, stream)
-        if workspace is None:
-            workspace = _empty(max(16, plan.grad_norm_workspace(count)), torch.uint8, device,
-                               stream)
-        out = _floats(norms, count, device, what, "norms")
-        each = _floats(param_norms, count * plan.num_params, device, what, "param_norms")
-        ws, ws_bytes = _workspace(workspace, grad_table, what)
-        table = _device_ptr(grad_table) + 8 * first * plan.num_params if device else None
-        _check(load_library().ddp_grad_norm(plan.handle, count, table, _plan_dtype(plan),
-                                            NORM[norm_type], out, each, ws, ws_bytes,
-                                            _stream(stream)), what)
+    if norms is None:
+        norms = _empty(count, _torch().float32, device, stream)
+    if workspace is None:
+        workspace = _empty(max(16, plan.grad_norm_workspace(count)), _torch().uint8, device,
+                           stream)
+    out = _floats(norms, count, device, what, "norms")
+    each = _floats(param_norms, count * plan.num_params, device, what, "param_norms")
+    ws, ws_bytes = _workspace(workspace, grad_table, what)
+    table = grad_table.data_ptr() + 8 * first * plan.num_params if device is not None else None
+    _check(load_library().ddp_grad_norm(plan.handle, count, table, _plan_dtype(plan),
+                                        NORM[norm_type], out, each, ws, ws_bytes,
+                                        _stream(stream)), what)
     return norms
 
 
@@ -734,14 +733,16 @@ def ddp_clip_grads(plan: Plan, grad_table, p: int, norms, max_norm: float, eps: 
     all-reduce), which are read once and written to all."""
     what = "ddp_clip_grads"
     _check_grad_table(grad_table, plan, p, what)
+    if _elsewhere(grad_table):
+        with _torch().cuda.device(grad_table.device):
+            return ddp_clip_grads(plan, grad_table, p, norms, max_norm, eps, replicated, stream)
     _check_norm_dtype(grad_table, what)
     device = grad_table.device if grad_table is not None else None
-    n = 1 if norms.numel() == 1 or replicated else p
-    with _on_device(grad_table):
-        _check(load_library().ddp_clip_grads(
-            plan.handle, p, _device_ptr(grad_table) if device else None, _plan_dtype(plan),
-            _floats(norms, n, device, what, "norms"), n, max_norm, eps, 1 if replicated else 0,
-            _stream(stream)), what)
+    n = 1 if replicated or norms.numel() == 1 else p
+    _check(load_library().ddp_clip_grads(
+        plan.handle, p, grad_table.data_ptr() if device is not None else None, _plan_dtype(plan),
+        _floats(norms, n, device, what, "norms"), n, max_norm, eps, 1 if replicated else 0,
+        _stream(stream)), what)
 
 
 def ddp_allreduce_buckets_norm(plan: Plan, first_bucket: int, n_buckets: int, grad_table, p: int,
@@ -752,15 +753,18 @@ def ddp_allreduce_buckets_norm(plan: Plan, first_bucket: int, n_buckets: int, gr
     ddp_grad_norm_finish joins them once every bucket has been reduced."""
     what = "ddp_allreduce_buckets_norm"
     _check_grad_table(grad_table, plan, p, what)
+    if _elsewhere(grad_table):
+        with _torch().cuda.device(grad_table.device):
+            return ddp_allreduce_buckets_norm(plan, first_bucket, n_buckets, grad_table, p,
+                                              workspace, norm_type, avg, tokens, stream)
     _check_norm_dtype(grad_table, what)
     st = CommStats()
-    with _on_device(grad_table):
-        ws, ws_bytes = _workspace(workspace, grad_table, what)
-        _check(load_library().ddp_allreduce_buckets_norm(
-            plan.handle, first_bucket, n_buckets, p,
-            _device_ptr(grad_table) if grad_table is not None else None, _plan_dtype(plan),
-            AVG[avg], _tokens(tokens, p), NORM[norm_type], ws, ws_bytes, _stream(stream),
-            ctypes.byref(st)), what)
+    ws, ws_bytes = _workspace(workspace, grad_table, what)
+    _check(load_library().ddp_allreduce_buckets_norm(
+        plan.handle, first_bucket, n_buckets, p,
+        grad_table.data_ptr() if grad_table is not None else None, _plan_dtype(plan),
+        AVG[avg], _tokens(tokens, p), NORM[norm_type], ws, ws_bytes, _stream(stream),
+        ctypes.byref(st)), what)
     return st
 
 
@@ -770,20 +774,20 @@ def ddp_grad_norm_finish(plan: Plan, workspace, norm=None, norm_type: str = "l2"
     with set_norm) left in `workspace`, as a float32 device tensor of one
     element (`norm`, or a new one); `param_norms`, if given, receives the
     n_params norms of the single parameters."""
-    import torch
-
     what = "ddp_grad_norm_finish"
     if workspace is None:
         raise ValueError(f"{what}: needs the workspace the partial sums were left in")
+    ws, ws_bytes = _workspace(workspace, None, what)
+    if _elsewhere(workspace):
+        with _torch().cuda.device(workspace.device):
+            return ddp_grad_norm_finish(plan, workspace, norm, norm_type, param_norms, stream)
     device = workspace.device
-    with _on_device(workspace):
-        if norm is None:
-            norm = _empty(1, torch.float32, device, stream)
-        ws, ws_bytes = _workspace(workspace, None, what)
-        _check(load_library().ddp_grad_norm_finish(
-            plan.handle, NORM[norm_type], _floats(norm, 1, device, what, "norm"),
-            _floats(param_norms, plan.num_params, device, what, "param_norms"), ws, ws_bytes,
-            _stream(stream)), what)
+    if norm is None:
+        norm = _empty(1, _torch().float32, device, stream)
+    _check(load_library().ddp_grad_norm_finish(
+        plan.handle, NORM[norm_type], _floats(norm, 1, device, what, "norm"),
+        _floats(param_norms, plan.num_params, device, what, "param_norms"), ws, ws_bytes,
+        _stream(stream)), what)
     return norm
 
 
@@ -795,17 +799,20 @@ def ddp_allreduce_clip(plan: Plan, grad_table, p: int, max_norm: float, norm, wo
     rank ends with min(1, max_norm / (norm + eps)) times the average."""
     what = "ddp_allreduce_clip"
     _check_grad_table(grad_table, plan, p, what)
+    if _elsewhere(grad_table):
+        with _torch().cuda.device(grad_table.device):
+            return ddp_allreduce_clip(plan, grad_table, p, max_norm, norm, workspace, eps,
+                                      norm_type, avg, tokens, param_norms, stream)
     _check_norm_dtype(grad_table, what)
     device = grad_table.device if grad_table is not None else None
     st = CommStats()
-    with _on_device(grad_table):
-        ws, ws_bytes = _workspace(workspace, grad_table, what)
-        _check(load_library().ddp_allreduce_clip(
-            plan.handle, p, _device_ptr(grad_table) if device else None, _plan_dtype(plan),
-            AVG[avg], _tokens(tokens, p), NORM[norm_type], max_norm, eps,
-            _floats(norm, 1, device, what, "norm"),
-            _floats(param_norms, plan.num_params, device, what, "param_norms"), ws, ws_bytes,
-            _stream(stream), ctypes.byref(st)), what)
+    ws, ws_bytes = _workspace(workspace, grad_table, what)
+    _check(load_library().ddp_allreduce_clip(
+        plan.handle, p, grad_table.data_ptr() if device is not None else None, _plan_dtype(plan),
+        AVG[avg], _tokens(tokens, p), NORM[norm_type], max_norm, eps,
+        _floats(norm, 1, device, what, "norm"),
+        _floats(param_norms, plan.num_params, device, what, "param_norms"), ws, ws_bytes,
+        _stream(stream), ctypes.byref(st)), what)
     return st
 
 
