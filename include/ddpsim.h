@@ -118,7 +118,8 @@ const char *ddp_version(void);
 
 /* Instrumentation. The next call on this thread of an entry point that
  * launches kernels (flatten / unflatten, the all-reduces and collectives,
- * the coalesced broadcast, and a reducer mark that launches a run) attaches
+ * the norm and clip calls, the coalesced broadcast, and a reducer mark that
+ * launches a run) attaches
  * `start` to the dispatch of its first kernel and `stop` to the dispatch of
  * its last kernel (hipExtLaunchKernel semantics), so
  * hipEventElapsedTime(start, stop) is exactly the device time of that
