@@ -181,7 +181,7 @@ __global__ __launch_bounds__(kBucketThreads) void bucket_allreduce_kernel(
 // wave leaves its tiles' part of the norm in partial (the sum of a run of one
 // parameter's tiles at its first tile, zeros at the others), or scales by the
 // coefficient.
-template <typename Tr, int G, int RB, int kMode, int NT>
+template <typename Tr, int G, int RB, int kMode, int NT, bool kNT>
 __global__ __launch_bounds__(64) void bucket_epilogue_kernel(
     const SegDesc *__restrict__ seg, const int32_t *__restrict__ tile_seg, int64_t map_stride,
     int32_t tile_base, int32_t n_tiles, int32_t n_params,
@@ -202,7 +202,7 @@ __global__ __launch_bounds__(64) void bucket_epilogue_kernel(
       const int64_t t1 = std::min((d.len + kTile - 1) / kTile, t + (end - tile));
       Epilogue<kMode, NT> epi;
       if constexpr (kMode == kSyncScale) epi.scale = clip_coefficient(*norm, max_norm, eps);
-      bucket_run<Tr, G, RB>(d, t, t1, tile, n_params, grads, p, div, epi);
+      bucket_run<Tr, G, RB, kNT>(d, t, t1, tile, n_params, grads, p, div, epi);
       const int32_t count = static_cast<int32_t>(t1 - t);
       if constexpr (kMode != kSyncScale) {
         join_wave(epi.sum);
@@ -252,22 +252,22 @@ struct BucketLaunch {
   WaveShape shape;
 };
 
-template <typename Tr, int G, int RB, int kMode, int NT>
+template <typename Tr, int G, int RB, int kMode, int NT, bool kNT = true>
 ddp_status launch_epilogue(const BucketLaunch &b, const SyncEpilogue &e, CallTimer &timer,
                            bool last) {
-  return launch_lds(bucket_epilogue_kernel<Tr, G, RB, kMode, NT>, b.grid, dim3(64), b.lds,
+  return launch_lds(bucket_epilogue_kernel<Tr, G, RB, kMode, NT, kNT>, b.grid, dim3(64), b.lds,
                     b.stream, timer, last, "bucket_epilogue_kernel launch", b.seg, b.tile_seg,
                     b.map_stride, b.tile0, b.tiles, b.n_params, b.grads, b.p, b.div, e.partial,
                     e.norm, e.max_norm, e.eps, e.runs);
 }
 
-template <typename Tr, int G, int RB, int kMode>
+template <typename Tr, int G, int RB, int kMode, bool kNT = true>
 ddp_status launch_norm_type(const BucketLaunch &b, const SyncEpilogue &e, CallTimer &timer,
                             bool last) {
   switch (e.norm_type) {
-    case DDP_NORM_L2: return launch_epilogue<Tr, G, RB, kMode, DDP_NORM_L2>(b, e, timer, last);
-    case DDP_NORM_L1: return launch_epilogue<Tr, G, RB, kMode, DDP_NORM_L1>(b, e, timer, last);
-    default: return launch_epilogue<Tr, G, RB, kMode, DDP_NORM_INF>(b, e, timer, last);
+    case DDP_NORM_L2: return launch_epilogue<Tr, G, RB, kMode, DDP_NORM_L2, kNT>(b, e, timer, last);
+    case DDP_NORM_L1: return launch_epilogue<Tr, G, RB, kMode, DDP_NORM_L1, kNT>(b, e, timer, last);
+    default: return launch_epilogue<Tr, G, RB, kMode, DDP_NORM_INF, kNT>(b, e, timer, last);
   }
 }
 
@@ -280,7 +280,15 @@ ddp_status launch_mode(const BucketLaunch &b, const SyncEpilogue &e, CallTimer &
   if (e.mode == kSyncNorm && !stays) {
     return launch_norm_type<Tr, G, RB, kSyncNorm>(b, e, timer, last);
   }
-  if (e.mode == kStageNorm) return launch_norm_type<Tr, G, RB, kStageNorm>(b, e, timer, last);
+  if (e.mode == kStageNorm) {
+    // Ordinary accesses where the gradients fit the cache: 36 us a call
+    // against 39 for 64 MB on 8 ranks (bf16 39 against 43), 17.5 against 18.3
+    // for 16 MB.
+    if (RB == 32 || e.cached) {
+      return launch_norm_type<Tr, G, RB, kStageNorm, false>(b, e, timer, last);
+    }
+    if constexpr (RB != 32) return launch_norm_type<Tr, G, RB, kStageNorm>(b, e, timer, last);
+  }
   if constexpr (RB != 32) {  // many loads in flight are for many ranks
     if (e.mode != kSyncScale) return launch_norm_type<Tr, G, RB, kFoldNorm>(b, e, timer, last);
     return launch_epilogue<Tr, G, RB, kSyncScale, DDP_NORM_L2>(b, e, timer, last);

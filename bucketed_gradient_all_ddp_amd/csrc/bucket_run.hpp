@@ -163,7 +163,8 @@ struct Epilogue {
 // bucket_tile for up to G consecutive tiles of one parameter, [t, t1) of its
 // own, the first of them tile `tile` of the plan, with an epilogue. One fetch
 // of the addresses serves them all, and G * RB loads are in flight.
-template <typename Tr, int G, int RB, typename Epi>
+// kNT: accesses that bypass the caches.
+template <typename Tr, int G, int RB, bool kNT, typename Epi>
 __device__ __forceinline__ void bucket_run(const SegDesc &d, int64_t t, int64_t t1, int32_t tile,
                                            int32_t n_params,
                                            const void *const *__restrict__ grads, int32_t p,
@@ -215,7 +216,7 @@ __device__ __forceinline__ void bucket_run(const SegDesc &d, int64_t t, int64_t 
   const int32_t c_last = chunk_of(d.offset, v1 * V - 1 - m, d.chunk);
   float acc[G][V];
   if (c_first == c_last) {
-    fold_vectors<Tr, G, RB, true>(lat, p, c_first, vi, ok, acc);
+    fold_vectors<Tr, G, RB, kNT>(lat, p, c_first, vi, ok, acc);
   } else {
 #pragma unroll
     for (int u = 0; u < G; ++u) {
@@ -233,7 +234,7 @@ __device__ __forceinline__ void bucket_run(const SegDesc &d, int64_t t, int64_t 
         }
         dist[e] = dd;
       }
-      fold_vector_per_lane<Tr, (RB > 8 ? RB : 8), true>(shifted, p, c0, dist, vi[u], ok[u], acc[u]);
+      fold_vector_per_lane<Tr, (RB > 8 ? RB : 8), kNT>(shifted, p, c0, dist, vi[u], ok[u], acc[u]);
     }
   }
 #pragma unroll
@@ -253,8 +254,8 @@ __device__ __forceinline__ void bucket_run(const SegDesc &d, int64_t t, int64_t 
       // past the caches: 0.73 ms for GPT-2 small on 8 ranks, 0.83 with
       // ordinary stores
       if (ok[u]) {
-        store_vec<true>(lat(a), vi[u], hi);
-        if constexpr (Tr::kStageRanks == 2) store_vec<true>(lat(ring_rank(a, 1, p)), vi[u], lo);
+        store_vec<kNT>(lat(a), vi[u], hi);
+        if constexpr (Tr::kStageRanks == 2) store_vec<kNT>(lat(ring_rank(a, 1, p)), vi[u], lo);
       }
     }
   }
@@ -267,7 +268,7 @@ __device__ __forceinline__ void bucket_run(const SegDesc &d, int64_t t, int64_t 
       void *dst = lat(ring_rank(rot, r, p));
 #pragma unroll
       for (int u = 0; u < G; ++u) {
-        if (ok[u]) store_vec<true>(dst, vi[u], y[u]);
+        if (ok[u]) store_vec<kNT>(dst, vi[u], y[u]);
       }
     }
   }

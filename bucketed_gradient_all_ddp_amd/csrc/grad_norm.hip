@@ -364,7 +364,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void small_sync_kernel(
     const SegDesc d = seg[tile_seg[tile_map_index(tile, map_stride)]];
     const int64_t t = tile - d.tile_begin;
     Epilogue<kStageNorm, NT> epi;
-    bucket_run<Tr, 1, 8>(d, t, t + 1, tile, n_params, ptrs, p, div, epi);
+    bucket_run<Tr, 1, 8, false>(d, t, t + 1, tile, n_params, ptrs, p, div, epi);
     join_wave(epi.sum);
     if ((threadIdx.x & 63) == 0) sums[tile] = epi.sum.part();
   }
@@ -798,7 +798,7 @@ extern "C" ddp_status ddp_allreduce_buckets_norm(const ddp_plan *plan, int32_t f
     s = check_scratch(what, workspace, workspace_bytes, ddp_sync_norm_workspace(plan));
   }
   if (s != DDP_OK) return s;
-  const SyncEpilogue epi = {kSyncNorm, norm_type, static_cast<double *>(workspace), nullptr, 0, 0, false};
+  const SyncEpilogue epi = {kSyncNorm, norm_type, static_cast<double *>(workspace), nullptr, 0, 0, false, false};
   return allreduce_buckets(plan, first_bucket, n_buckets, p, d_grad_ptrs, dtype, avg_mode, tokens,
                            stream, stats, DDPSIM_BUCKET_MAX_WORKGROUPS, &epi, &timer);
 }
@@ -877,7 +877,7 @@ extern "C" ddp_status ddp_allreduce_clip(const ddp_plan *plan, int32_t p,
                                                  eps, d_norm, d_param_norms, stream, timer);
   } else {
     SyncEpilogue epi = {staged ? kStageNorm : kFoldNorm, norm_type, sums, d_norm, max_norm, eps,
-                        runs_per_xcd(t, p)};
+                        runs_per_xcd(t, p), int64_t(p) * t.elems * t.elem_bytes <= kCacheBytes};
     if (nb > 0) {
       s = allreduce_buckets(plan, 0, nb, p, d_grad_ptrs, dtype, avg_mode, tokens, stream, stats,
                             DDPSIM_BUCKET_MAX_WORKGROUPS, &epi, &timer, false);

@@ -241,7 +241,8 @@ struct SyncEpilogue {
   double *partial;    // one value per plan tile
   const float *norm;  // device
   float max_norm, eps;
-  bool runs;  // kStageNorm: runs_per_xcd
+  bool runs;    // kStageNorm: runs_per_xcd
+  bool cached;  // kStageNorm: the ranks' gradients fit the Infinity Cache
 };
 
 // ddp_allreduce_buckets with an optional cap on its workgroups (0: one per
