@@ -1,7 +1,7 @@
 """GPU: every launch form of the all-reduce with its norm and with clipping:
 several tiles per wave (few ranks, many tiles), 32 and 8 rank loads in flight
-(many ranks), tiles in runs per XCD and stores past the caches (large sets), and
-values that are not finite.
+(many ranks), tiles in runs per XCD and stores past the caches (large sets),
+values that are not finite, and each call's outputs in a captured graph.
 
 Norms: as in test_gpu_grad_norm.py, but the sets have up to 2^25.1 elements: a
 sum of N terms in 64 bits is off by at most N 2^-53 of itself (2^-27 here),
@@ -409,3 +409,85 @@ def test_past_the_caches_same_phase(p, avg, form, bf16):
     arena.copy_(keep)
     ddp.ddp_clip_grads(plan, table, p, norms[:1], 100.0, replicated=True)
     assert torch.equal(arena, whole(keep[0, :total].float() * own[:1]))
+
+
+# ---------------------------------------------------------------------------
+# Every output of every call in one captured graph
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_captured_outputs_apart(oracle, bf16):
+    """Three forms of the clip (one workgroup; joined by the second pass; by a
+    launch, with parameter norms) and the norm's own calls, each with outputs
+    and a workspace of its own, replayed on fresh gradients."""
+    p = 3
+    shapes = {"small": [700, 3, 0, 300, 9], "inline": [30_000, 17, 0, 5],
+              "joined": [30_000, 17, 0, 40_000, 5], "norm": [30_000, 17, 0, 5]}
+    sets = {k: Ranks(p, v, bf16, "odd", oracle, seed=171) for k, v in shapes.items()}
+    plans = {k: _plan(s, 96 * 1024, 8 * 1024) for k, s in sets.items()}
+    ws = {k: _workspace(q.sync_norm_workspace())[0] for k, q in plans.items()}
+    ws["own"] = _workspace(plans["norm"].grad_norm_workspace(p))[0]
+    out = {k: torch.empty(1, device="cuda") for k in shapes}
+    out["own"] = torch.empty(p, device="cuda")
+    each = {k: torch.empty(len(v), device="cuda") for k, v in shapes.items() if k != "inline"}
+    each["own"] = torch.empty(p, len(shapes["norm"]), device="cuda")
+    for s in sets.values():
+        s.upload()
+    inputs = {}
+    for seed in (1, 2, 3):
+        for k, v in shapes.items():
+            fresh = Ranks(p, v, bf16, "odd", oracle, seed=180 + seed)
+            fresh.upload()
+            inputs[seed, k] = fresh.dev
+
+    def fill(seed):
+        for k, s in sets.items():
+            s.dev.copy_(inputs[seed, k])
+        for t in list(out.values()) + list(each.values()):
+            t.fill_(-1.0)
+
+    def work():
+        for k in ("small", "inline", "joined"):
+            ddp.ddp_allreduce_clip(plans[k], sets[k].table, p, 0.5, out[k], ws[k], avg="world",
+                                   param_norms=each.get(k))
+        q, s = plans["norm"], sets["norm"]
+        ddp.ddp_grad_norm(q, s.table, p, out["own"], param_norms=each["own"], workspace=ws["own"])
+        ddp.ddp_allreduce_buckets_norm(q, 0, q.num_buckets, s.table, p, ws["norm"], avg="world")
+        ddp.ddp_grad_norm_finish(q, ws["norm"], out["norm"], param_norms=each["norm"])
+
+    def state():
+        torch.cuda.synchronize()
+        return {**{("grads", k): s.dev.clone() for k, s in sets.items()},
+                **{("norm", k): t.clone() for k, t in out.items()},
+                **{("each", k): t.clone() for k, t in each.items()}}
+
+    want = {}
+    for seed in (1, 2, 3):
+        fill(seed)
+        work()
+        want[seed] = state()
+        for k, s in sets.items():
+            s.values = Ranks(p, shapes[k], bf16, "odd", oracle, seed=180 + seed).values
+            avgs = s.averages("world", None, 96 * 1024, 8 * 1024)
+            _close(out[k].cpu().numpy()[0], _norm64([avgs], "l2"), k)
+            if k in each:
+                _close(each[k].cpu().numpy(), [_norm64([v], "l2") for v in s.split(avgs)], k)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        work()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        work()
+    for seed in (1, 2, 3, 2):
+        fill(seed)
+        torch.cuda.synchronize()
+        g.replay()
+        for key, t in state().items():
+            a, b = t, want[seed][key]
+            kind = torch.int16 if a.dtype == torch.bfloat16 else torch.int32
+            assert torch.equal(a.view(kind), b.view(kind)), (seed, key)
+        x = torch.randn(1 << 20, device="cuda")
+        (x * 2).sum().item()
