@@ -489,7 +489,8 @@ __global__ __launch_bounds__(64 * kMaxFanoutWaves) void clip_fanout_kernel(
   }
 }
 
-// Plan, rank count, type and table of a norm or clip call.
+// Plan, rank count, type and table of a norm or clip call. Whether the plan
+// has its descriptor table is asked last (check_uploaded).
 ddp_status check_call(const char *what, const ddp_plan *plan, int32_t p, const void *d_grad_ptrs,
                       int32_t dtype, PlanTiles *t) {
   if (!plan_tiles(plan, t)) return fail(DDP_EINVAL, "%s: plan is NULL", what);
@@ -501,13 +502,15 @@ ddp_status check_call(const char *what, const ddp_plan *plan, int32_t p, const v
     return fail(DDP_EINVAL, "%s: dtype has %d-byte elements, the plan %d", what, eb,
                 t->elem_bytes);
   }
-  if (t->seg_p == 0) {
-    return fail(DDP_ENOTREADY, "%s: call ddp_plan_upload_segments first", what);
-  }
   if (t->tiles > 0 && d_grad_ptrs == nullptr) {
     return fail(DDP_EINVAL, "%s: gradient pointer table is NULL", what);
   }
   return DDP_OK;
+}
+
+ddp_status check_uploaded(const char *what, const PlanTiles &t) {
+  if (t.seg_p != 0) return DDP_OK;
+  return fail(DDP_ENOTREADY, "%s: call ddp_plan_upload_segments first", what);
 }
 
 ddp_status check_norm_type(const char *what, int32_t norm_type) {
@@ -525,17 +528,30 @@ ddp_status check_bound(const char *what, float max_norm, float eps) {
   return DDP_OK;
 }
 
-ddp_status check_out(const char *what, const float *d_norms, const float *d_param_norms) {
+// n norms and n_each parameters' norms, and the workspace of `need` bytes
+// that their sums lie in: the last join writes norms while it reads sums, so
+// that none of the three may share memory with another.
+ddp_status check_out(const char *what, const float *d_norms, int64_t n, const float *d_param_norms,
+                     int64_t n_each, const void *workspace, size_t bytes, size_t need) {
   if (d_norms == nullptr) return fail(DDP_EINVAL, "%s: d_norms is NULL", what);
   if (reinterpret_cast<uintptr_t>(d_norms) % 4 != 0 ||
       reinterpret_cast<uintptr_t>(d_param_norms) % 4 != 0) {
     return fail(DDP_EALIGN, "%s: the norms are not 4-byte aligned", what);
   }
+  ddp_status s = check_workspace(what, workspace, bytes, need, nullptr, 0, 0);
+  if (s != DDP_OK) return s;
+  n_each = d_param_norms != nullptr ? n_each : 0;
+  const auto overlap = [](const void *a, int64_t na, const void *b, int64_t nb) {
+    return na > 0 && nb > 0 && ranges_overlap(a, na, b, nb);
+  };
+  const int64_t ws = static_cast<int64_t>(need);
+  if (overlap(d_norms, 4 * n, workspace, ws) || overlap(d_param_norms, 4 * n_each, workspace, ws)) {
+    return fail(DDP_EALIAS, "%s: the norms overlap the workspace", what);
+  }
+  if (overlap(d_norms, 4 * n, d_param_norms, 4 * n_each)) {
+    return fail(DDP_EALIAS, "%s: d_norms and d_param_norms overlap", what);
+  }
   return DDP_OK;
-}
-
-ddp_status check_scratch(const char *what, const void *workspace, size_t bytes, size_t need) {
-  return check_workspace(what, workspace, bytes, need, nullptr, 0, 0);
 }
 
 template <int NT>
@@ -750,10 +766,11 @@ extern "C" ddp_status ddp_grad_norm(const ddp_plan *plan, int32_t p,
   PlanTiles t;
   ddp_status s = check_call(what, plan, p, d_grad_ptrs, dtype, &t);
   if (s == DDP_OK) s = check_norm_type(what, norm_type);
-  if (s == DDP_OK) s = check_out(what, d_norms, d_param_norms);
   if (s == DDP_OK) {
-    s = check_scratch(what, workspace, workspace_bytes, ddp_grad_norm_workspace(plan, p));
+    s = check_out(what, d_norms, p, d_param_norms, int64_t(p) * t.n_params, workspace,
+                  workspace_bytes, ddp_grad_norm_workspace(plan, p));
   }
+  if (s == DDP_OK) s = check_uploaded(what, t);
   if (s != DDP_OK) return s;
   return launch_norm_type(dtype, norm_type, t, p, d_grad_ptrs, static_cast<double *>(workspace),
                           d_norms, d_param_norms, stream, timer, true);
@@ -768,8 +785,9 @@ extern "C" ddp_status ddp_clip_grads(const ddp_plan *plan, int32_t p, void *cons
   const char *what = "ddp_clip_grads";
   PlanTiles t;
   ddp_status s = check_call(what, plan, p, d_grad_ptrs, dtype, &t);
-  if (s == DDP_OK) s = check_out(what, d_norms, nullptr);
+  if (s == DDP_OK) s = check_out(what, d_norms, n_norms, nullptr, 0, nullptr, 0, 0);
   if (s == DDP_OK) s = check_bound(what, max_norm, eps);
+  if (s == DDP_OK) s = check_uploaded(what, t);
   if (s != DDP_OK) return s;
   if (replicated != 0 && replicated != 1) {
     return fail(DDP_EINVAL, "%s: replicated must be 0 or 1", what);
@@ -795,10 +813,12 @@ extern "C" ddp_status ddp_allreduce_buckets_norm(const ddp_plan *plan, int32_t f
   const char *what = "ddp_allreduce_buckets_norm";
   ddp_status s = check_norm_type(what, norm_type);
   if (s == DDP_OK) {
-    s = check_scratch(what, workspace, workspace_bytes, ddp_sync_norm_workspace(plan));
+    s = check_workspace(what, workspace, workspace_bytes, ddp_sync_norm_workspace(plan), nullptr,
+                        0, 0);
   }
   if (s != DDP_OK) return s;
-  const SyncEpilogue epi = {kSyncNorm, norm_type, static_cast<double *>(workspace), nullptr, 0, 0, false, false};
+  const SyncEpilogue epi = {kSyncNorm, norm_type, static_cast<double *>(workspace), nullptr, 0, 0,
+                            false, false};
   return allreduce_buckets(plan, first_bucket, n_buckets, p, d_grad_ptrs, dtype, avg_mode, tokens,
                            stream, stats, DDPSIM_BUCKET_MAX_WORKGROUPS, &epi, &timer);
 }
@@ -811,14 +831,12 @@ extern "C" ddp_status ddp_grad_norm_finish(const ddp_plan *plan, int32_t norm_ty
   const char *what = "ddp_grad_norm_finish";
   PlanTiles t;
   if (!plan_tiles(plan, &t)) return fail(DDP_EINVAL, "%s: plan is NULL", what);
-  if (t.seg_p == 0) {
-    return fail(DDP_ENOTREADY, "%s: call ddp_plan_upload_segments first", what);
-  }
   ddp_status s = check_norm_type(what, norm_type);
-  if (s == DDP_OK) s = check_out(what, d_norm, d_param_norms);
   if (s == DDP_OK) {
-    s = check_scratch(what, workspace, workspace_bytes, ddp_sync_norm_workspace(plan));
+    s = check_out(what, d_norm, 1, d_param_norms, t.n_params, workspace, workspace_bytes,
+                  ddp_sync_norm_workspace(plan));
   }
+  if (s == DDP_OK) s = check_uploaded(what, t);
   if (s != DDP_OK) return s;
   return launch_tile_finish(t, norm_type, static_cast<double *>(workspace), d_norm,
                             d_param_norms, stream, timer, true);
@@ -838,10 +856,11 @@ extern "C" ddp_status ddp_allreduce_clip(const ddp_plan *plan, int32_t p,
   ddp_status s = check_call(what, plan, p, d_grad_ptrs, dtype, &t);
   if (s == DDP_OK) s = check_norm_type(what, norm_type);
   if (s == DDP_OK) s = check_bound(what, max_norm, eps);
-  if (s == DDP_OK) s = check_out(what, d_norm, d_param_norms);
   if (s == DDP_OK) {
-    s = check_scratch(what, workspace, workspace_bytes, ddp_sync_norm_workspace(plan));
+    s = check_out(what, d_norm, 1, d_param_norms, t.n_params, workspace, workspace_bytes,
+                  ddp_sync_norm_workspace(plan));
   }
+  if (s == DDP_OK) s = check_uploaded(what, t);
   if (s != DDP_OK) return s;
   if (t.seg_p != p) {
     return fail(DDP_ENOTREADY, "%s: call ddp_plan_upload_segments with p=%d first", what, p);

@@ -337,8 +337,10 @@ size_t ddp_grad_norm_workspace(const ddp_plan *plan, int32_t p);
  *   workspace      ddp_grad_norm_workspace(plan, p) bytes, 16-byte aligned;
  *                  written before it is read; calls that may overlap in time
  *                  need workspaces of their own
+ * d_norms, d_param_norms and the workspace must not overlap one another, nor
+ * a gradient (which is not checked).
  * Errors: DDP_EINVAL, DDP_ERANGE (p), DDP_ENOTREADY (no descriptor table),
- * DDP_EALIGN, DDP_EWORKSPACE. */
+ * DDP_EALIGN, DDP_EWORKSPACE, DDP_EALIAS. */
 ddp_status ddp_grad_norm(const ddp_plan *plan, int32_t p,
                          const void *const *d_grad_ptrs, int32_t dtype,
                          int32_t norm_type, float *d_norms,
@@ -409,7 +411,7 @@ ddp_status ddp_grad_norm_finish(const ddp_plan *plan, int32_t norm_type,
  * ranks' for bf16), so that after a DDP_EHIP the gradients are undefined. The
  * descriptor table must be the one for p. The stats describe the ring
  * schedules, with the device traffic of this call. Errors: as
- * ddp_allreduce_buckets_norm and ddp_clip_grads. */
+ * ddp_allreduce_buckets_norm, ddp_grad_norm_finish and ddp_clip_grads. */
 ddp_status ddp_allreduce_clip(const ddp_plan *plan, int32_t p,
                               void *const *d_grad_ptrs, int32_t dtype,
                               int32_t avg_mode, const int64_t *tokens,

@@ -1,0 +1,52 @@
+"""Refusals of the norm and clip calls on calls that are well formed argument
+by argument. Host-side only: nothing is launched, no pointer dereferenced."""
+import ctypes
+
+import bucketed_gradient_all_ddp_amd as ddp
+from bucketed_gradient_all_ddp_amd.binding import load_library
+
+FAKE = ctypes.c_void_p(0x100000000)
+OUT, EACH, WS = 0x200000000, 0x300000000, 0x400000000
+BIG = 1 << 40
+EALIAS, ENOTREADY = 4, 6
+
+
+def _p(address):
+    return ctypes.c_void_p(address)
+
+
+def test_norms_that_share_memory():
+    """The last join writes norms while other workgroups still read sums and
+    write other norms: outputs and workspace have to lie apart."""
+    L = load_library()
+    sizes, p = [100, 0, 5000], 4
+    plan = ddp.ddp_bucket_plan(sizes, 4, 1024, 256)  # (no descriptor table: asked last)
+    need, need_sync = plan.grad_norm_workspace(p), plan.sync_norm_workspace()
+    assert need >= 64 and need_sync >= 64
+
+    def norm(out, each, ws):
+        return L.ddp_grad_norm(plan.handle, p, FAKE, 0, 0, _p(out), _p(each), _p(ws), need, None)
+
+    def finish(out, each, ws):
+        return L.ddp_grad_norm_finish(plan.handle, 0, _p(out), _p(each), _p(ws), need_sync, None)
+
+    def clip(out, each, ws):
+        return L.ddp_allreduce_clip(plan.handle, p, FAKE, 0, 0, None, 0, 1.0, 1e-6, _p(out),
+                                    _p(each), _p(ws), need_sync, None, None)
+
+    for call, ranks, size in ((norm, p, need), (finish, 1, need_sync), (clip, 1, need_sync)):
+        n, n_each = 4 * ranks, 4 * ranks * len(sizes)  # bytes
+        assert call(OUT, EACH, WS) == ENOTREADY
+        assert call(OUT, 0, WS) == ENOTREADY
+        # side by side
+        assert call(WS - n, WS + size, WS) == ENOTREADY
+        assert call(WS + size, WS - n_each, WS) == ENOTREADY
+        assert call(OUT, OUT + n, WS) == ENOTREADY and call(OUT, OUT - n_each, WS) == ENOTREADY
+        for out in (WS, WS + 4, WS + size - 4, WS - n + 4):
+            assert call(out, 0, WS) == EALIAS and call(out, EACH, WS) == EALIAS
+            assert b"workspace" in L.ddp_last_error()
+        for each in (WS, WS + size - 4, WS - n_each + 4):
+            assert call(OUT, each, WS) == EALIAS
+        for each in (OUT, OUT + n - 4, OUT - n_each + 4):
+            assert call(OUT, each, WS) == EALIAS
+            assert b"d_param_norms" in L.ddp_last_error()
