@@ -635,6 +635,16 @@ def _elsewhere(tensor) -> bool:
     return tensor is not None and tensor.get_device() != _torch()._C._cuda_getDevice()
 
 
+def _check_plan_device(plan: Plan, tensor, what: str) -> None:
+    """The kernels run on the tensor's device and read the plan's descriptor
+    table there."""
+    if tensor is None or plan._segments is None:
+        return  # (without a table the library refuses the call)
+    if plan._segments.get_device() != tensor.get_device():
+        raise ValueError(f"{what}: the plan's descriptor table is on {plan._segments.device}, the "
+                         f"call's tensors are on {tensor.device}: upload_segments to that device")
+
+
 def _empty(n: int, dtype, device, stream):
     """Device memory for use on `stream` (None: the current stream)."""
     import torch
@@ -706,6 +716,7 @@ def ddp_grad_norm(plan: Plan, grad_table, p: int, norms=None, norm_type: str = "
             return ddp_grad_norm(plan, grad_table, p, norms, norm_type, param_norms, ranks,
                                  workspace, stream)
     _check_norm_dtype(grad_table, what)
+    _check_plan_device(plan, grad_table, what)
     first, count = (0, p) if ranks is None else ranks
     if first < 0 or count < 1 or first + count > p:
         raise ValueError(f"{what}: ranks {first}..{first + count - 1} outside 0..{p - 1}")
@@ -737,6 +748,7 @@ def ddp_clip_grads(plan: Plan, grad_table, p: int, norms, max_norm: float, eps: 
         with _torch().cuda.device(grad_table.device):
             return ddp_clip_grads(plan, grad_table, p, norms, max_norm, eps, replicated, stream)
     _check_norm_dtype(grad_table, what)
+    _check_plan_device(plan, grad_table, what)
     device = grad_table.device if grad_table is not None else None
     n = 1 if replicated or norms.numel() == 1 else p
     _check(load_library().ddp_clip_grads(
@@ -758,6 +770,7 @@ def ddp_allreduce_buckets_norm(plan: Plan, first_bucket: int, n_buckets: int, gr
             return ddp_allreduce_buckets_norm(plan, first_bucket, n_buckets, grad_table, p,
                                               workspace, norm_type, avg, tokens, stream)
     _check_norm_dtype(grad_table, what)
+    _check_plan_device(plan, grad_table, what)
     st = CommStats()
     ws, ws_bytes = _workspace(workspace, grad_table, what)
     _check(load_library().ddp_allreduce_buckets_norm(
@@ -781,6 +794,7 @@ def ddp_grad_norm_finish(plan: Plan, workspace, norm=None, norm_type: str = "l2"
     if _elsewhere(workspace):
         with _torch().cuda.device(workspace.device):
             return ddp_grad_norm_finish(plan, workspace, norm, norm_type, param_norms, stream)
+    _check_plan_device(plan, workspace, what)
     device = workspace.device
     if norm is None:
         norm = _empty(1, _torch().float32, device, stream)
@@ -804,6 +818,7 @@ def ddp_allreduce_clip(plan: Plan, grad_table, p: int, max_norm: float, norm, wo
             return ddp_allreduce_clip(plan, grad_table, p, max_norm, norm, workspace, eps,
                                       norm_type, avg, tokens, param_norms, stream)
     _check_norm_dtype(grad_table, what)
+    _check_plan_device(plan, grad_table, what)
     device = grad_table.device if grad_table is not None else None
     st = CommStats()
     ws, ws_bytes = _workspace(workspace, grad_table, what)

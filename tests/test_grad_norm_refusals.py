@@ -1,8 +1,13 @@
 """Refusals of the norm and clip calls on calls that are well formed argument
 by argument. Host-side only: nothing is launched, no pointer dereferenced."""
 import ctypes
+from types import SimpleNamespace
+
+import pytest
+import torch
 
 import bucketed_gradient_all_ddp_amd as ddp
+from bucketed_gradient_all_ddp_amd import binding
 from bucketed_gradient_all_ddp_amd.binding import load_library
 
 FAKE = ctypes.c_void_p(0x100000000)
@@ -50,3 +55,39 @@ def test_norms_that_share_memory():
         for each in (OUT, OUT + n - 4, OUT - n_each + 4):
             assert call(OUT, each, WS) == EALIAS
             assert b"d_param_norms" in L.ddp_last_error()
+
+
+def _cpu_table(p, numels):
+    t = torch.zeros(p * len(numels), dtype=torch.int64)
+    t._ddp_ranks, t._ddp_numel, t._ddp_elem_bytes = p, tuple(numels), 4
+    t._ddp_dtypes = frozenset([torch.float32])
+    return t
+
+
+def test_descriptor_table_on_another_device(monkeypatch):
+    """The kernels read the plan's descriptor table where they run, on the
+    gradients' device: a table uploaded to another device is refused. (Host
+    tensors stand for device tensors; the plan has no table in the library, so
+    nothing is launched.)"""
+    monkeypatch.setattr(binding, "_device_ptr", lambda t: t.data_ptr())
+    monkeypatch.setattr(binding, "_elsewhere", lambda t: False)
+    monkeypatch.setattr(binding, "_stream", lambda s: None)
+    monkeypatch.setattr(binding, "_floats", lambda t, *a: None if t is None else t.data_ptr())
+    sizes, p = [10, 20], 2
+    plan = ddp.ddp_bucket_plan(sizes, 4, 1024, 256)
+    table, norm = _cpu_table(p, sizes), torch.zeros(1)
+    ws = torch.zeros(64, dtype=torch.int64)
+    calls = [
+        lambda: ddp.ddp_grad_norm(plan, table, p, workspace=ws),
+        lambda: ddp.ddp_clip_grads(plan, table, p, norm, 1.0),
+        lambda: ddp.ddp_allreduce_buckets_norm(plan, 0, plan.num_buckets, table, p, ws),
+        lambda: ddp.ddp_grad_norm_finish(plan, ws, norm),
+        lambda: ddp.ddp_allreduce_clip(plan, table, p, 1.0, norm, ws),
+    ]
+    for call in calls:
+        plan._segments = SimpleNamespace(device="cuda:1", get_device=lambda: 1)
+        with pytest.raises(ValueError, match="descriptor table is on cuda:1"):
+            call()
+        plan._segments = SimpleNamespace(device="cpu", get_device=lambda: -1)
+        with pytest.raises(ddp.DDPError, match="ENOTREADY"):
+            call()
