@@ -883,6 +883,14 @@ class Reducer:
         ptr, nbytes = _workspace(workspace, self._table, "Reducer.set_norm")
         _check(load_library().ddp_reducer_set_norm(self._h, NORM[norm_type], ptr, nbytes),
                "ddp_reducer_set_norm")
+        if workspace is not None:
+            # allocated on one stream, written on the communication stream,
+            # perhaps still when a pass is given up: the memory is not reused
+            # before the launches there have run
+            comm = self.comm_stream
+            if not hasattr(comm, "cuda_stream"):
+                comm = _torch().cuda.ExternalStream(int(comm), device=workspace.device)
+            workspace.record_stream(comm)
         self._workspace = workspace  # kept alive
 
     def ready_order(self) -> List[int]:

@@ -491,3 +491,35 @@ def test_captured_outputs_apart(oracle, bf16):
             assert torch.equal(a.view(kind), b.view(kind)), (seed, key)
         x = torch.randn(1 << 20, device="cuda")
         (x * 2).sum().item()
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_abandoned_pass_keeps_the_workspace(oracle, handle):
+    """A pass that is given up with launches still queued on the communication
+    stream: the sums' memory is handed to nobody else before they have run."""
+    p, sizes = 2, [30_000, 17, 0, 5]
+    s = Ranks(p, sizes, False, "odd", oracle, seed=190)
+    plan = _plan(s, 96 * 1024, 8 * 1024)
+    s.upload()
+    avgs = s.averages("world", None, 96 * 1024, 8 * 1024)
+    comm = torch.cuda.Stream()
+    red = ddp.Reducer(plan, p, s.table, avg="world",
+                      comm_stream=comm.cuda_stream if handle else comm)
+    big = torch.zeros(2, 1 << 28, device="cuda")
+    torch.cuda.synchronize()
+    ws = torch.empty(plan.sync_norm_workspace(), dtype=torch.uint8, device="cuda")
+    address, nbytes = ws.data_ptr(), ws.numel()
+    red.set_norm(ws)
+    red.prepare()
+    with torch.cuda.stream(comm):  # a few milliseconds of copies ahead of the launches
+        for _ in range(60):
+            big[1].copy_(big[0])
+    for i in range(len(sizes)):
+        red.mark_ready(i)
+    del ws, red
+    others = [torch.full((nbytes,), 9, dtype=torch.uint8, device="cuda") for _ in range(20)]
+    assert all(t.data_ptr() != address for t in others)
+    assert not comm.query()  # the launches had not run yet
+    torch.cuda.synchronize()
+    assert all(bool((t == 9).all()) for t in others)
+    s.check(avgs, "all-reduce")
