@@ -39,10 +39,25 @@ constexpr int kSmallWaves = 16;  // waves of the one-workgroup kernels
 // Most tiles of a rank whose norms one workgroup takes: 7 to 8 us a call up
 // to 256, where two launches take 10; 512 in bf16 14.
 constexpr int kSmallNormTiles = 256;
-// Most tiles of an all-reduce with clipping by one workgroup, one per wave: 7
-// to 8 us a call where several workgroups take 10 to 11; with 32 tiles the
-// waves' second folds cost more than the launch they save.
+// The all-reduce with clipping of a small set by one workgroup, a tile per
+// wave, against the launches of several workgroups: two, or three where the
+// parameters' norms are wanted (us a call, fp32; bf16 takes up to 2 more with
+// few ranks and 6 with 64):
+//   ranks                      8           16          32          64
+//   tiles                    1   16      8   16      8   16      8   16
+//   one workgroup           6.5  7.6    8.4  9.7   11.5 16.5   18.2 27.3
+//   two launches            9.8 10.1   10.5 10.1   12.1 12.2   16.0 16.1
+//   one, parameters' norms  6.9  8.4    9.0 10.2   12.1 17.1   18.8 27.9
+//   three launches         13.0 13.4   13.8 13.2   15.0 15.1   18.8 19.3
+// A wave folds 8 ranks at a time, so that with many ranks its batches follow
+// one another in the one compute unit that the launch fills, and more than 8
+// waves then wait for one another. With 32 tiles the waves' second folds cost
+// more than the launch they save.
 constexpr int kSmallSyncTiles = kSmallWaves;
+bool small_sync(int64_t tiles, int32_t p, bool param_norms) {
+  if (tiles > (p <= 16 ? kSmallSyncTiles : kSmallSyncTiles / 2)) return false;
+  return p <= 32 || param_norms;
+}
 // Most tile sums that the spreading pass joins by itself: 11 us a call
 // against 14 with a launch for the join.
 constexpr int kInlineTiles = 1024;
@@ -887,7 +902,7 @@ extern "C" ddp_status ddp_allreduce_clip(const ddp_plan *plan, int32_t p,
                          timer, false);
     if (s != DDP_OK) return s;
     s = launch_clip(dtype, t, 1, d_grad_ptrs, d_norm, 1, max_norm, eps, false, stream, timer);
-  } else if (staged && t.tiles > 0 && t.tiles <= kSmallSyncTiles) {
+  } else if (staged && t.tiles > 0 && small_sync(t.tiles, p, d_param_norms != nullptr)) {
     for (int32_t b = 0; b < nb; ++b) add_ring_stats(p, ddp_plan_bucket_numel(plan, b), stats);
     s = dtype == DDP_F32
             ? launch_small_sync_type<F32Traits>(norm_type, t, p, d_grad_ptrs, div, max_norm, eps,

@@ -228,12 +228,27 @@ MANY = [40_001, 256 * 40, 1, 2, 3, 1023, 1025, 4096 + 5, 255, 257, 20_000, 5, 0,
     (9, "world", "l1", True), (17, "world", "l2", True), (32, "none", "l2", False),
     (33, "tokens", "inf", True), (64, "world", "l2", False), (64, "none", "l1", True)])
 def test_many_ranks(oracle, p, avg, kind, param_norms, bf16, layout):
-    """More tiles than one workgroup takes, fewer than 4,096: 32 rank loads in
+    """More tiles than one workgroup takes, few for the chip: 32 rank loads in
     flight, in one batch or two; joined by the second pass (no parameter
     norms) or by a launch."""
     assert 16 < _tiles(MANY, bf16) <= 1024
     s = Ranks(p, MANY, bf16, layout, oracle, seed=130 + p)
     _check_both(s, kind, avg, param_norms=param_norms)
+
+
+@pytest.mark.parametrize("layout", ["aligned", "odd", "mixed"])
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("p,sizes", [
+    (9, [700, 3, 0, 1300, 9, 256]), (16, [700, 3, 0, 1300, 9, 256]), (17, [700, 3, 0, 9]),
+    (17, [700, 3, 0, 1300, 9, 256]), (33, [700, 3, 0, 9]), (64, [700, 3, 0, 1300, 9, 256]),
+    (64, [700, 3, 0, 9])])
+def test_few_tiles(oracle, p, sizes, bf16, layout):
+    """Up to 16 tiles: by one workgroup or by several, with and without the
+    parameters' norms."""
+    assert _tiles(sizes, bf16) <= 16
+    s = Ranks(p, sizes, bf16, layout, oracle, seed=135 + p)
+    _check_both(s, "l2", "world", param_norms=False)
+    _check_both(s, "l1", "tokens")
 
 
 @pytest.mark.parametrize("layout", ["aligned", "odd", "mixed"])
