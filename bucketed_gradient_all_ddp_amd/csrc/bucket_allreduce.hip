@@ -222,11 +222,18 @@ __global__ __launch_bounds__(64) void bucket_epilogue_kernel(
 // on GPT-2 small fp32, 1 / 2 / 4 tiles per wave: 0.34 / 0.19 / 0.12 ms for
 // one rank, 0.41 / 0.28 / 0.23 for 2, 0.45 / 0.33 / 0.35 for 3, 0.47 / 0.41 /
 // 0.42 for 4, 0.49 / 0.51 / 0.53 for 5.
-// With many ranks and few tiles, one wave's folds follow one another with
-// the chip nearly empty: 32 loads in flight instead of 8 (64 ranks of 131,849
-// elements: 17.7 us against 19.5).
+// With more than 8 ranks and tiles for few waves, one wave's folds follow one
+// another with the chip nearly empty: 32 loads in flight instead of 8. All-reduce
+// with norm, fp32, us of 32 / 8 loads:
+//   tiles         500          1000          2000          4000
+//   16 ranks   10.7 / 11.3   11.8 / 11.8   17.0 / 17.1   32.9 / 32.2
+//   32 ranks   14.8 / 16.8   19.4 / 20.6   33.0 / 32.3   65.1 / 64.9
+//   64 ranks   25.6 / 30.0   36.6 / 38.4   65.9 / 65.5    130 / 131
+// and with clipping much the same (both passes, 4000 tiles of 16 ranks: 38.6 /
+// 35.1). The registers of 32 loads leave 2 waves per SIMD, those of 8 loads 5
+// (bf16 4).
 constexpr int64_t kFullTiles = 16384;  // waves that fill the chip twice over
-constexpr int64_t kFewTiles = 4096;
+constexpr int64_t kFewTiles = 1536;
 struct WaveShape {
   int32_t tiles, loads;
 };

@@ -255,7 +255,7 @@ def test_few_tiles(oracle, p, sizes, bf16, layout):
 @pytest.mark.parametrize("bf16", [False, True])
 @pytest.mark.parametrize("p", [9, 33])
 def test_many_ranks_many_tiles(oracle, p, bf16, layout):
-    """From 4,096 tiles on: 8 rank loads in flight, in p / 8 batches."""
+    """Tiles for a full chip: 8 rank loads in flight, in p / 8 batches."""
     sizes = MANY + [(4100 * (512 if bf16 else 256)) + 1]
     assert _tiles(sizes, bf16) >= 4096
     s = Ranks(p, sizes, bf16, layout, oracle, seed=140 + p)
