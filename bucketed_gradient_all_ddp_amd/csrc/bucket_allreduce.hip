@@ -26,11 +26,13 @@
 // The same pass can also take the norm of the averaged gradient, one partial
 // sum per tile, from the fp32 values before they are rounded to the
 // gradients' type, and it can scale them by the clip coefficient of a norm
-// in device memory (SyncMode). The norm costs the all-reduce nothing that can
-// be measured: GPT-2 small, 8 ranks, 1.27 to 1.31 ms a launch on the boxes
-// where the plain launch takes 1.27 to 1.29. As the first pass of an
-// all-reduce with clipping (8 ranks read, one written) it runs at 6.1 TB/s,
-// 0.73 ms, and at 6.4 TB/s on two Llama-7B layers in bf16 (two written).
+// in device memory (SyncMode). In fp32 the norm costs the all-reduce nothing
+// that can be measured: GPT-2 small, 8 ranks, 1.27 to 1.31 ms a launch on the
+// boxes where the plain launch takes 1.27 to 1.29; in bf16 2%: two Llama-7B
+// layers, 8 ranks, 2.14 ms (6.05 TB/s) where the plain launch takes 2.09. As
+// the first pass of an all-reduce with clipping (8 ranks read, one written) it
+// runs at 6.1 TB/s, 0.73 ms, and at 6.1 to 6.4 TB/s on two Llama-7B layers in
+// bf16 (two written).
 #include <algorithm>
 
 #include "bucket_run.hpp"
@@ -402,7 +404,9 @@ ddp_status allreduce_buckets(const ddp_plan *plan, int32_t first_bucket, int32_t
   // buckets by 3-4%; 6 per CU starved the channels (5.2). A pass that stores
   // to one or two ranks or none has half as many: bounded at 11 it read the 8
   // ranks' GPT-2 gradients at 5.3 TB/s, at 14, 18 and 24 per CU at 6.5, 6.9
-  // and 6.8 (Llama layers in bf16 4.7, and 5.9, 6.3, 6.3).
+  // and 6.8 (Llama layers in bf16 4.7, and 5.9, 6.3, 6.3). The kernels'
+  // registers bound it too: one tile a wave at 20 per CU in fp32 and 16 in
+  // bf16, four tiles a wave at 20 and 12, 32 loads in flight at 8.
   const bool reads = epi != nullptr && (epi->mode == kFoldNorm || epi->mode == kStageNorm);
   const size_t lds = residency_lds(
       fold_residency(reads ? DDPSIM_FOLD_WGS_PER_CU : DDPSIM_BUCKET_WGS_PER_CU, p * shape.tiles));

@@ -288,12 +288,12 @@ __device__ __forceinline__ void bucket_run(const SegDesc &d, int64_t t, int64_t 
 // two workgroups, whose halves an L2 has to put together: ordinary stores,
 // and neighbouring tiles on one XCD (runs_per_xcd), take 0.94 ms instead of
 // 1.07 for 300 odd tensors of that size, and 0.13 instead of 0.21 for 300 on
-// 64 ranks. What is left, 6.1 TB/s for one stream in and eight out, is the
-// latency of a workgroup's chain of loads (tile map, descriptor, addresses,
-// source): bounding residency slowed it (0.96 ms at 8 workgroups per CU),
-// and so did groups of 2 and 4 tiles a wave (0.76, 0.77) and a grid-stride
-// loop that fetches the next tiles ahead (0.98). With 2 or 8 destinations a
-// wave instead of 4 it took 0.97 and 0.77.
+// 64 ranks. One stream in and eight out runs at 5.9 to 6.0 TB/s, bf16 (two in)
+// at 5.4 to 5.6, where the fan-out copy reaches 6.4 to 6.6; what holds it is
+// not shown by a counter. On fp32 bounding residency slowed it (0.96 ms at 8
+// workgroups per CU), and so did groups of 2 and 4 tiles a wave (0.76, 0.77)
+// and a grid-stride loop that fetches the next tiles ahead (0.98). With 2 or 8
+// destinations a wave instead of 4 it took 0.97 and 0.77.
 template <typename Tr, bool kStaged, bool kBarrier>
 __device__ __forceinline__ void spread_tile(const SegDesc &d, int64_t tile, int32_t n_params,
                                             const void *const *__restrict__ ptrs, int32_t p,

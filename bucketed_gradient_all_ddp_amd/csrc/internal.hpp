@@ -233,7 +233,9 @@ enum SyncMode : int32_t {
   kStageNorm = 4
 };
 #ifndef DDPSIM_FOLD_WGS_PER_CU
-#define DDPSIM_FOLD_WGS_PER_CU 18  // workgroups resident per CU of kFoldNorm
+// workgroups resident per CU of kFoldNorm and kStageNorm (the bf16 kernels'
+// registers admit 16)
+#define DDPSIM_FOLD_WGS_PER_CU 18
 #endif
 struct SyncEpilogue {
   int32_t mode;

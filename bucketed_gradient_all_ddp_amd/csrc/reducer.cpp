@@ -145,7 +145,8 @@ extern "C" ddp_status ddp_reducer_set_norm(ddp_reducer *r, int32_t norm_type, vo
   ddp_status s = check_workspace(what, workspace, workspace_bytes,
                                  ddp_sync_norm_workspace(r->plan), nullptr, 0, 0);
   if (s != DDP_OK) return s;
-  r->norm = SyncEpilogue{kSyncNorm, norm_type, static_cast<double *>(workspace), nullptr, 0, 0, false, false};
+  r->norm = SyncEpilogue{kSyncNorm, norm_type, static_cast<double *>(workspace), nullptr, 0, 0,
+                         false, false};
   return DDP_OK;
 }
 

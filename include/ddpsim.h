@@ -370,14 +370,18 @@ ddp_status ddp_clip_grads(const ddp_plan *plan, int32_t p,
                           float max_norm, float eps, int32_t replicated,
                           hipStream_t stream);
 
-/* Workspace bytes of the three entry points below (0 for a NULL plan). */
+/* Workspace bytes of the three entry points below (0 for a NULL plan). Calls
+ * that may overlap in time need workspaces of their own, but for the runs of
+ * buckets of one norm. */
 size_t ddp_sync_norm_workspace(const ddp_plan *plan);
 
 /* ddp_allreduce_buckets, and in the same pass the norm's partial sums of the
  * averaged gradients of those buckets, left in `workspace` (16-byte aligned,
  * ddp_sync_norm_workspace(plan) bytes, each bucket's sums at a place of
  * their own). The gradients end with the bits of ddp_allreduce_buckets; the
- * norm is that of the fp32 averages, before bf16 rounds them. Once every
+ * norm is that of the fp32 averages, before bf16 rounds them. The stats are
+ * those of ddp_allreduce_buckets (2 p n_b bytes-per-element of device traffic;
+ * a single rank without a division is only read, half of that). Once every
  * bucket of the plan has been through it (in one run or several, on any
  * streams ordered before the call), ddp_grad_norm_finish joins the sums with
  * the same norm_type. Errors: as ddp_allreduce_buckets, plus DDP_EWORKSPACE
